@@ -1,0 +1,509 @@
+// attend_shared.cu -- HCA attention over a prefix that a batch shares, entries of each sequence's own and the
+// window, and the weights that the own entries receive: entry points, and the CUDA-core kernels
+// (fp32, and shapes that the tensor-core kernels do not take).
+//
+//     out = sum_r p_r v_r,  p = softmax_r(q . v_r / sqrt(d)),  lse = log sum_r e^{q . v_r / sqrt(d)}
+//
+// over the prefix, the own entries that the query sees, and the window.  Every query of the batch sees
+// the whole prefix, so for it the queries and heads of all sequences are just rows of one matrix: they are
+// taken in groups that ignore where one sequence ends, and a prefix row that has been loaded serves a
+// whole group.  The own entries and the window go by query.  The two kinds of work are cut into pieces
+// along the keys, each with its running maximum m, sum l and unnormalised output, and joined at the
+// end: out = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i.
+//
+// CUDA-core kernels: a block takes 16 rows (4 per warp) and tiles of 32 keys staged as fp32 in shared
+// memory.  For the scores a lane is a key; for the output it is a slice of d, and each probability is
+// broadcast from the lane that has it.  4 rows per warp mean 16 FMAs per 16-byte read of a key, which the
+// FMA pipes bound.  Products and sums in fp32 throughout.
+#include "common.cuh"
+#include "internal.h"
+#include "shared.h"
+
+#include <type_traits>
+
+namespace v4a {
+namespace {
+
+constexpr int kRowsB = 16;    // rows per block
+constexpr int kKeys = 32;     // keys per tile
+constexpr int kThreads = 128;
+constexpr int kRw = 4;        // rows per warp
+
+struct SimtPlan {
+    int groups;            // row groups of the prefix part
+    int splits;            // its pieces per group
+    int head_tiles;        // row groups per query of the own part
+    int own_splits;        // its pieces
+    int own_keys;          // own_rows + window
+    long long rows;        // batch * n_q * heads
+};
+
+template <typename T, int D>
+struct Tile {
+    float k[kKeys][D + 4];
+    float q[kRowsB][D];
+    int ok[kKeys];
+};
+
+// stage one row of d elements (null: zeros) as fp32, by the lanes of one warp
+template <typename T, int D>
+__device__ __forceinline__ void stage_row(float* dst, const T* src, int lane) {
+    for (int c = lane * 8; c < D; c += 256) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (src) Vec8<T>::load_nc(src + c, f);
+        *reinterpret_cast<float4*>(dst + c) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(dst + c + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// this lane's key against the warp's four rows
+template <int D>
+__device__ __forceinline__ void dots(const float* key, const float (*q)[D], float (&s)[kRw]) {
+#pragma unroll
+    for (int r = 0; r < kRw; ++r) s[r] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(key + c);
+#pragma unroll
+        for (int r = 0; r < kRw; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(&q[r][c]);
+            s[r] = fmaf(x.x, k.x, s[r]);
+            s[r] = fmaf(x.y, k.y, s[r]);
+            s[r] = fmaf(x.z, k.z, s[r]);
+            s[r] = fmaf(x.w, k.w, s[r]);
+        }
+    }
+}
+
+// One piece: 16 rows against a range of keys.  Blocks below groups * splits take prefix pieces, the others
+// own-and-window pieces.  A piece's rows go to part_ml / part_o [piece][16] (see piece_of).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, SimtPlan p, float2* part_ml, float* part_o) {
+    griddep_wait();  // everything before this kernel on the stream has finished
+    griddep_launch_dependents();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Tile<T, D>& sm = *reinterpret_cast<Tile<T, D>*>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long piece = blockIdx.x;
+    const long long n_pre = (long long)p.groups * p.splits;
+    const bool pre = piece < n_pre;
+    long long row0, k0, k1, t = 0, seen = 0;
+    int n_rows, b = 0, count = 0;
+    if (pre) {
+        const long long g = piece / p.splits;
+        const int sp = (int)(piece % p.splits);
+        row0 = g * kRowsB;
+        n_rows = (int)(p.rows - row0 < kRowsB ? p.rows - row0 : kRowsB);
+        const long long per = (a.n_prefix + p.splits - 1) / p.splits;
+        k0 = sp * per;
+        k1 = k0 + per < a.n_prefix ? k0 + per : a.n_prefix;
+    } else {
+        long long i = piece - n_pre;
+        const int sp = (int)(i % p.own_splits);
+        i /= p.own_splits;
+        const int ht = (int)(i % p.head_tiles);
+        const long long query = i / p.head_tiles;
+        b = (int)(query / a.n_q);
+        row0 = query * a.heads + ht * kRowsB;
+        n_rows = a.heads - ht * kRowsB < kRowsB ? a.heads - ht * kRowsB : kRowsB;
+        t = seq_len(a, b) - a.n_q + query % a.n_q;
+        seen = seen_entries(a, t);
+        count = own_slots(a, b);
+        const int per = (p.own_keys + p.own_splits - 1) / p.own_splits;
+        k0 = (long long)sp * per;
+        k1 = k0 + per < p.own_keys ? k0 + per : p.own_keys;
+        if (!has_candidates(a, t)) k1 = k0;
+    }
+    for (int r = warp; r < kRowsB; r += kThreads / 32)
+        stage_row<T, D>(sm.q[r], r < n_rows ? static_cast<const T*>(a.q) + (row0 + r) * D : nullptr, lane);
+    constexpr int kE = D / 32;  // output elements per lane and row, in groups of 4 (2 for D = 64)
+    constexpr int kV = kE < 4 ? kE : 4;
+    float o[kRw][kE], m_run[kRw], l_run[kRw];
+#pragma unroll
+    for (int r = 0; r < kRw; ++r) {
+        m_run[r] = -INFINITY;
+        l_run[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[r][e] = 0.f;
+    }
+    const float scale = kLog2eF / sqrtf((float)D);
+    for (long long base = k0; base < k1; base += kKeys) {
+        __syncthreads();
+        for (int i = warp; i < kKeys; i += kThreads / 32) {
+            const long long c = base + i;
+            const T* src = nullptr;
+            if (c < k1) {
+                if (pre) {
+                    src = static_cast<const T*>(a.prefix) + c * D;
+                } else if (c < a.own_rows) {
+                    if (c < count && slot_seen(a, b, (int)c, seen)) src = static_cast<const T*>(a.own) + ((long long)b * a.own_rows + c) * D;
+                } else {
+                    const long long pos = t - a.window + 1 + (c - a.own_rows);
+                    if (pos >= 0) src = static_cast<const T*>(a.ring) + ((long long)b * a.ring_rows + pos % a.ring_rows) * D;
+                }
+            }
+            stage_row<T, D>(sm.k[i], src, lane);
+            if (lane == 0) sm.ok[i] = src != nullptr;
+        }
+        __syncthreads();
+        float s[kRw];
+        dots<D>(sm.k[lane], &sm.q[warp * kRw], s);
+        const bool ok = sm.ok[lane];
+#pragma unroll
+        for (int r = 0; r < kRw; ++r) {
+            const float x = ok ? s[r] * scale : -INFINITY;
+            const float mt = group_max<32>(x), m_new = fmaxf(m_run[r], mt);
+            const float msub = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = exp2f(m_run[r] - msub);
+            s[r] = exp2f(x - msub);
+            l_run[r] = l_run[r] * alpha + s[r];  // each lane's own share of the row sum
+            m_run[r] = m_new;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[r][e] *= alpha;
+        }
+        for (int j = 0; j < kKeys; ++j) {
+            float v[kE], pj[kRw];
+#pragma unroll
+            for (int g = 0; g < kE / kV; ++g) {
+                const float* vp = &sm.k[j][g * 32 * kV + lane * kV];
+#pragma unroll
+                for (int e = 0; e < kV; ++e) v[g * kV + e] = vp[e];
+            }
+#pragma unroll
+            for (int r = 0; r < kRw; ++r) pj[r] = __shfl_sync(0xffffffffu, s[r], j);
+#pragma unroll
+            for (int r = 0; r < kRw; ++r)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) o[r][e] = fmaf(pj[r], v[e], o[r][e]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRw; ++r) {
+        const float l = group_sum<32>(l_run[r]);
+        const long long pr = piece * kRowsB + warp * kRw + r;
+        if (lane == 0) part_ml[pr] = make_float2(isnan(l) ? NAN : m_run[r], l);  // a NaN logit poisons its row
+        float* op = part_o + pr * D;
+#pragma unroll
+        for (int g = 0; g < kE / kV; ++g)
+#pragma unroll
+            for (int e = 0; e < kV; ++e) op[g * 32 * kV + lane * kV + e] = o[r][g * kV + e];
+    }
+}
+
+// one block per row (query, head): joins its pieces
+__global__ void __launch_bounds__(128) shared_join_kernel(SharedArgs a, SimtPlan p, const float2* part_ml, const float* part_o) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long row = blockIdx.x;
+    const int d = a.d;
+    const long long query = row / a.heads;
+    const int h = (int)(row % a.heads), b = (int)(query / a.n_q);
+    const long long t = seq_len(a, b) - a.n_q + query % a.n_q;
+    const bool live = has_candidates(a, t);
+    const int n_pre = p.groups ? p.splits : 0, n = n_pre + p.own_splits;
+    // row of piece i in part_ml / part_o
+    auto piece_row = [&](int i) -> long long {
+        if (i < n_pre) return ((row / kRowsB) * p.splits + i) * kRowsB + row % kRowsB;
+        const long long own = (long long)p.groups * p.splits + (query * p.head_tiles + h / kRowsB) * p.own_splits + (i - n_pre);
+        return own * kRowsB + h % kRowsB;
+    };
+    if (threadIdx.x == 0 && h == 0 && query % a.n_q == 0) report_sequence(a, b);
+    float mmax = -INFINITY;
+    if (live)
+        for (int i = 0; i < n; ++i) {
+            const float m = part_ml[piece_row(i)].x;
+            mmax = isnan(m) || isnan(mmax) ? NAN : fmaxf(mmax, m);
+        }
+    float l = 0.f;
+    if (mmax != -INFINITY) {
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = part_ml[piece_row(i)];
+            if (ml.x != -INFINITY) l += exp2f(ml.x - mmax) * ml.y;
+        }
+        if (a.sink) l += exp2f(a.sink[h] * kLog2eF - mmax);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+    if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (mmax + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
+    const int r0 = d - a.rope_dims;
+    for (int e = threadIdx.x * 2; e < d; e += 256) {
+        float x = 0.f, y = 0.f;
+        if (mmax != -INFINITY) {
+            for (int i = 0; i < n; ++i) {
+                const long long pr = piece_row(i);
+                const float ms = part_ml[pr].x;
+                if (ms == -INFINITY) continue;  // its output was never accumulated
+                const float w = exp2f(ms - mmax);
+                const float2 v = *reinterpret_cast<const float2*>(part_o + pr * d + e);
+                x = fmaf(w, v.x, x);
+                y = fmaf(w, v.y, y);
+            }
+        }
+        x *= inv;
+        y *= inv;
+        if (a.rope_dims > 0 && e >= r0 && live) {
+            float s, c;
+            rope_sincos(t, (e - r0) >> 1, a.rope_dims, a.rope_base, &s, &c);
+            const float u = x;
+            x = fmaf(u, c, -y * s);
+            y = fmaf(u, s, y * c);
+        }
+        if (a.out_dtype == V4A_F32) {
+            *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * d + e) = make_float2(x, y);
+        } else {
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + row * d + e) = __floats2bfloat162_rn(x, y);
+        }
+    }
+}
+
+// Weights: a block takes 32 own slots of one sequence and runs over the sequence's rows (query, head), 16 at
+// a time.  A warp's lane is a slot; the four warps' sums are added in a fixed order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) weights_kernel(SharedArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Tile<T, D>& sm = *reinterpret_cast<Tile<T, D>*>(smem_raw);
+    __shared__ float sums[kThreads / 32][kKeys];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, i0 = blockIdx.x * kKeys, count = own_slots(a, b);
+    if (blockIdx.x == 0 && threadIdx.x == 0) report_sequence(a, b);
+    if (i0 >= count) return;
+    const long long len = seq_len(a, b);
+    for (int i = warp; i < kKeys; i += kThreads / 32)
+        stage_row<T, D>(sm.k[i], i0 + i < count ? static_cast<const T*>(a.own) + ((long long)b * a.own_rows + i0 + i) * D : nullptr, lane);
+    const int slot = i0 + lane;
+    long long e = -1;  // this lane's entry
+    if (slot < count) e = a.own_entry ? (long long)a.own_entry[(long long)b * a.own_rows + slot] : a.n_prefix + slot;
+    const float scale = kLog2eF / sqrtf((float)D);
+    const int n = a.n_q * a.heads;
+    const long long row0 = (long long)b * n;
+    float got = 0.f;
+    for (int base = 0; base < n; base += kRowsB) {
+        __syncthreads();
+        for (int r = warp; r < kRowsB; r += kThreads / 32)
+            stage_row<T, D>(sm.q[r], base + r < n ? static_cast<const T*>(a.q) + (row0 + base + r) * D : nullptr, lane);
+        __syncthreads();
+        float s[kRw];
+        dots<D>(sm.k[lane], &sm.q[warp * kRw], s);
+#pragma unroll
+        for (int r = 0; r < kRw; ++r) {
+            const int i = base + warp * kRw + r;
+            if (i >= n) continue;
+            const float lse = a.lse[row0 + i];
+            const long long seen = seen_entries(a, len - a.n_q + i / a.heads);
+            if (e >= 0 && e < seen && lse != -INFINITY) got += exp2f(fmaf(s[r], scale, -lse * kLog2eF));
+        }
+    }
+    sums[warp][lane] = got;
+    __syncthreads();
+    if (warp == 0 && slot < count) {
+        const long long at = (long long)b * a.own_rows + slot;
+        const float total = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+        a.weights_out[at] = a.decay == 0.f ? total : fmaf(a.decay, a.weights_in[at], total);
+    }
+}
+
+SimtPlan simt_plan(const SharedArgs& a) {
+    SimtPlan p;
+    p.rows = (long long)a.batch * a.n_q * a.heads;
+    p.groups = a.n_prefix > 0 ? (int)((p.rows + kRowsB - 1) / kRowsB) : 0;
+    p.head_tiles = (a.heads + kRowsB - 1) / kRowsB;
+    p.own_keys = a.own_rows + a.window;
+    const long long queries = (long long)a.batch * a.n_q;
+    auto cut = [](long long pieces, long long keys) {  // enough blocks for the SMs, 32 keys each at least
+        long long want = pieces > 0 ? (4LL * kNumSMs + pieces - 1) / pieces : 1, most = (keys + kKeys - 1) / kKeys;
+        if (want > most) want = most;
+        return (int)(want < 1 ? 1 : want > 1024 ? 1024 : want);
+    };
+    p.splits = p.groups ? cut(p.groups, a.n_prefix) : 0;
+    p.own_splits = p.own_keys > 0 ? cut(queries * p.head_tiles, p.own_keys) : 0;
+    return p;
+}
+
+long long simt_pieces(const SharedArgs& a, const SimtPlan& p) {
+    return (long long)p.groups * p.splits + (long long)a.batch * a.n_q * p.head_tiles * p.own_splits;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t simt_bytes(const SharedArgs& a) {
+    const long long n = simt_pieces(a, simt_plan(a)) * kRowsB;
+    return align256(n * sizeof(float2)) + n * a.d * sizeof(float);
+}
+
+template <typename T, int D>
+cudaError_t simt_attend(const SharedArgs& a, void* ws, cudaStream_t st) {
+    const SimtPlan p = simt_plan(a);
+    const long long pieces = simt_pieces(a, p);
+    float2* ml = static_cast<float2*>(ws);
+    float* po = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(pieces * kRowsB * sizeof(float2)));
+    auto* kernel = shared_split_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Tile<T, D>));
+    if (e == cudaSuccess && pieces > 0)
+        e = launch_pdl(kernel, dim3((unsigned)pieces), dim3(kThreads), sizeof(Tile<T, D>), st, a, p, ml, po);
+    if (e == cudaSuccess)
+        e = launch_pdl(shared_join_kernel, dim3((unsigned)p.rows), dim3(128), 0, st, a, p, (const float2*)ml, (const float*)po);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <typename T, int D>
+cudaError_t simt_weights(const SharedArgs& a, cudaStream_t st) {
+    auto* kernel = weights_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Tile<T, D>));
+    if (e == cudaSuccess)
+        e = launch_pdl(kernel, dim3((unsigned)((a.own_rows + kKeys - 1) / kKeys), (unsigned)a.batch), dim3(kThreads),
+                       sizeof(Tile<T, D>), st, a);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <typename F>
+cudaError_t by_shape(const SharedArgs& a, F f) {
+    const bool f32 = a.dtype == V4A_F32;
+    switch (a.d) {
+    case 64: return f32 ? f(0.f, std::integral_constant<int, 64>()) : f(__nv_bfloat16(), std::integral_constant<int, 64>());
+    case 128: return f32 ? f(0.f, std::integral_constant<int, 128>()) : f(__nv_bfloat16(), std::integral_constant<int, 128>());
+    case 256: return f32 ? f(0.f, std::integral_constant<int, 256>()) : f(__nv_bfloat16(), std::integral_constant<int, 256>());
+    default: return f32 ? f(0.f, std::integral_constant<int, 512>()) : f(__nv_bfloat16(), std::integral_constant<int, 512>());
+    }
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// the checks that both calls share; fills everything but the outputs
+v4a_status shared_args(const char* what, const void* q, const v4a_shared_cache* c, v4a_dtype dtype, int* dev_status,
+                       const v4a_shape* s, SharedArgs* a) {
+    if (!s || !c) return report(V4A_ERR_INVALID_ARG, "%s: shape or cache is NULL", what);
+    if (s->batch < 0 || s->n_q < 1 || s->m < 1 || s->ctx_len < 1 || s->n_q > s->ctx_len)
+        return report(V4A_ERR_INVALID_ARG, "%s: need batch >= 0, m >= 1, 1 <= n_q <= ctx_len", what);
+    if ((long long)s->batch * s->n_q > 65535) return report(V4A_ERR_UNSUPPORTED, "%s: batch * n_q must be <= 65535", what);
+    if (s->heads < 1 || s->heads > 1024) return report(V4A_ERR_INVALID_ARG, "%s: heads must be in 1..1024", what);
+    if (s->d != 64 && s->d != 128 && s->d != 256 && s->d != 512)
+        return report(V4A_ERR_UNSUPPORTED, "%s: d must be 64, 128, 256 or 512", what);
+    if (dtype != V4A_F32 && dtype != V4A_BF16) return report(V4A_ERR_UNSUPPORTED, "%s: dtype must be F32 or BF16", what);
+    if (c->n_prefix < 0 || c->n_prefix > s->ctx_len / s->m || c->n_prefix > 0x3fffffffLL)
+        return report(V4A_ERR_INVALID_ARG, "%s: n_prefix must be in 0..ctx_len / m", what);
+    if (c->own_rows < 0 || c->own_rows > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: own_rows out of range", what);
+    if (s->window < 0 || s->window > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: window must be >= 0", what);
+    if (s->batch > 0 && (!q || (c->own_rows > 0 && !c->own))) return report(V4A_ERR_INVALID_ARG, "%s: q and own are required", what);
+    if (!aligned(q, 16) || !aligned(c->own, 16) || !aligned(c->prefix, 16) || !aligned(c->ring, 16))
+        return report(V4A_ERR_INVALID_ARG, "%s: q, prefix, own and ring must be 16-byte aligned", what);
+    if (!aligned(c->own_count, 4) || !aligned(c->own_entry, 4) || !aligned(c->ctx_lens, 8) || !aligned(dev_status, 4))
+        return report(V4A_ERR_INVALID_ARG, "%s: own_count, own_entry, ctx_lens or dev_status misaligned", what);
+    *a = SharedArgs{};
+    a->q = q;
+    a->prefix = c->prefix;
+    a->own = c->own;
+    a->ring = c->ring;
+    a->own_count = c->own_count;
+    a->own_entry = c->own_entry;
+    a->ctx_lens = c->ctx_lens;
+    a->dev_status = dev_status;
+    a->dtype = dtype;
+    a->batch = s->batch;
+    a->n_q = s->n_q;
+    a->heads = s->heads;
+    a->d = s->d;
+    a->m = s->m;
+    a->own_rows = c->own_rows;
+    a->ring_rows = c->ring_rows;
+    a->n_prefix = c->n_prefix;
+    a->ctx_len = s->ctx_len;
+    return V4A_OK;
+}
+
+v4a_status from_cuda(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? V4A_OK : report(V4A_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace v4a
+
+extern "C" {
+
+v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, void* out, v4a_dtype out_dtype,
+                                 float* lse, v4a_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 int* dev_status, const v4a_attend_ext* ext, const v4a_shape* shape, void* stream) {
+    using namespace v4a;
+    const char* what = "v4a_hca_attend_shared";
+    SharedArgs a;
+    const v4a_status st = shared_args(what, q, cache, dtype, dev_status, shape, &a);
+    if (st != V4A_OK) return st;
+    a.window = shape->window;
+    if (a.batch == 0) return V4A_OK;
+    if (!out) return report(V4A_ERR_INVALID_ARG, "%s: out is required", what);
+    if (a.n_prefix > 0 && !a.prefix) return report(V4A_ERR_INVALID_ARG, "%s: prefix is required", what);
+    if (out_dtype != V4A_F32 && !(out_dtype == V4A_BF16 && dtype == V4A_BF16))
+        return report(V4A_ERR_UNSUPPORTED, "%s: out_dtype must be F32, or BF16 with BF16 inputs", what);
+    if (!aligned(out, 16) || !aligned(lse, 4)) return report(V4A_ERR_INVALID_ARG, "%s: out (16 bytes) or lse (4 bytes) misaligned", what);
+    if (a.window > 0 && (!a.ring || a.ring_rows < 1 || (long long)a.ring_rows < (long long)a.window + a.n_q - 1))
+        return report(V4A_ERR_INVALID_ARG, "%s: the ring of %d rows cannot hold the window (%d + %d - 1)", what,
+                      a.ring ? a.ring_rows : 0, a.window, a.n_q);
+    if (ext) {
+        if (ext->rope_dims < 0 || ext->rope_dims > a.d || (ext->rope_dims & 1))
+            return report(V4A_ERR_INVALID_ARG, "%s: rope_dims must be even and in 0..d", what);
+        if (ext->rope_dims > 0 && !(ext->rope_base > 0.f)) return report(V4A_ERR_INVALID_ARG, "%s: rope_base must be > 0", what);
+        if (!aligned(ext->sink, 4)) return report(V4A_ERR_INVALID_ARG, "%s: sink must be 4-byte aligned", what);
+        a.sink = ext->sink;
+        a.rope_dims = ext->rope_dims;
+        a.rope_base = ext->rope_base;
+    }
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse;
+    const size_t need = v4a_shared_workspace_size(shape, a.n_prefix, a.own_rows, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return report(V4A_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (!aligned(workspace, 256)) return report(V4A_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    cudaStream_t s = (cudaStream_t)stream;
+    if (dev_status) {
+        const cudaError_t e = launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, s);
+        if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
+    }
+    return from_cuda(by_shape(a, [&](auto t, auto d) { return simt_attend<decltype(t), decltype(d)::value>(a, workspace, s); }), what);
+}
+
+size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_prefix, int own_rows, v4a_dtype dtype) {
+    using namespace v4a;
+    if (!shape || shape->batch < 1 || shape->n_q < 1 || shape->heads < 1 || shape->heads > 1024 || shape->d < 64 ||
+        shape->d > 512 || shape->window < 0 || n_prefix < 0 || own_rows < 0 || (long long)shape->batch * shape->n_q > 65535)
+        return 0;
+    SharedArgs a = {};
+    a.batch = shape->batch;
+    a.n_q = shape->n_q;
+    a.heads = shape->heads;
+    a.d = shape->d;
+    a.window = shape->window;
+    a.own_rows = own_rows;
+    a.n_prefix = n_prefix;
+    a.dtype = dtype;
+    return simt_bytes(a);
+}
+
+v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, const float* lse, const float* weights_in,
+                              float* weights_out, float decay, v4a_dtype dtype, int* dev_status, const v4a_shape* shape,
+                              void* stream) {
+    using namespace v4a;
+    const char* what = "v4a_attend_weights";
+    SharedArgs a;
+    const v4a_status st = shared_args(what, q, cache, dtype, dev_status, shape, &a);
+    if (st != V4A_OK) return st;
+    if (!(decay >= 0.f) || isinf(decay)) return report(V4A_ERR_INVALID_ARG, "%s: decay must be finite and >= 0", what);
+    if (a.batch == 0) return V4A_OK;
+    if (!lse || (a.own_rows > 0 && (!weights_out || (decay != 0.f && !weights_in))))
+        return report(V4A_ERR_INVALID_ARG, "%s: lse, weights_out and (with decay > 0) weights_in are required", what);
+    if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4))
+        return report(V4A_ERR_INVALID_ARG, "%s: lse or weights misaligned", what);
+    a.lse = const_cast<float*>(lse);  // read only
+    a.weights_in = weights_in;
+    a.weights_out = weights_out;
+    a.decay = decay;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (dev_status) {
+        const cudaError_t e = launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, s);
+        if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
+    }
+    if (a.own_rows == 0) return V4A_OK;
+    return from_cuda(by_shape(a, [&](auto t, auto d) { return simt_weights<decltype(t), decltype(d)::value>(a, s); }), what);
+}
+
+}  // extern "C"

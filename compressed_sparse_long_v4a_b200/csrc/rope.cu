@@ -1,0 +1,317 @@
+// rope.cu -- rotary positions: y = s R(+-p f_k) x on R of a row's d dims.
+//
+// Pair k of a row at position p turns by the angle p f_k, f_k = base^(-2k/R) (scaled for long contexts
+// on the host).  What is read and written once bounds it: 2 d elements per row (2 R in place), against
+// 3 flops per rotated element.  The angles are per token, not per row, so a block takes one token (or
+// a part of its rows), works out the token's R/2 (cos, sin) once into shared memory, and streams rows:
+// one thread per 8 elements (16 bytes of bf16), four in flight.  A decode step has few tokens; their
+// rows are then cut over several blocks, each with its own copy of the 32 angles.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace v4a {
+namespace {
+
+constexpr int kMaxStreams = 8;
+constexpr int kMaxPairs = 256;
+constexpr int kThreads = 256;
+
+struct RopeStream {
+    const void* x;
+    void* out;
+    int heads, d, off;
+    int rot, row_items;  // items of a row: rotated ones first, then the copied chunks
+    int parts;           // blocks per token
+    long long xb, xt, xh, ob, ot, oh;
+};
+
+struct RopeArgs {
+    RopeStream s[kMaxStreams];
+    double f_hi[kMaxPairs];  // turns (not radians) per position, as a sum of two
+    float f_lo[kMaxPairs];
+    int n, n_tok, pairs, half, inverse;
+    float scale;
+    const int64_t* positions;
+    long long pos_stride, pos0, pos_step;
+};
+
+// cos and sin of p f, f = f_hi + f_lo turns per position: the product as an exact sum of two doubles, so
+// the fraction of a turn keeps more than 24 bits for |p| up to 2^40
+__device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
+    const double hi = p * f_hi;
+    const double lo = fma(p, f_hi, -hi) + p * (double)f_lo;
+    const double frac = (hi - rint(hi)) + lo;
+    float s, c;
+    sincospif((float)(2.0 * frac), &s, &c);
+    return make_float2(c, s);
+}
+
+__device__ __forceinline__ void block_table(const RopeArgs& a, int b, int t, float2* cs) {
+    const int k = threadIdx.x;
+    if (k < a.pairs) {
+        const long long p = a.positions ? a.positions[b * a.pos_stride + t] : a.pos0 + t * a.pos_step;
+        float2 v = turn((double)p, a.f_hi[k], a.f_lo[k]);
+        cs[k] = make_float2(v.x * a.scale, (a.inverse ? -v.y : v.y) * a.scale);
+    }
+    __syncthreads();
+}
+
+// the stream and the part of it that this block takes
+__device__ __forceinline__ int which_stream(const RopeArgs& a, int& part) {
+    part = blockIdx.y;
+    int k = 0;
+    while (part >= a.s[k].parts) part -= a.s[k++].parts;
+    return k;
+}
+
+// Rows, offsets and strides in multiples of 8 elements: an item is one 8-element chunk, or, in the half
+// layout, the two chunks that a rotated item pairs up.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ float2 cs[kMaxPairs];
+    griddep_wait();  // everything before this kernel on the stream has finished
+    int part;
+    const RopeStream& s = a.s[which_stream(a, part)];
+    const int b = blockIdx.x / a.n_tok, t = blockIdx.x % a.n_tok;
+    const T* xt = static_cast<const T*>(s.x) + b * s.xb + t * s.xt;
+    T* ot = static_cast<T*>(s.out) + b * s.ob + t * s.ot;
+    const int R = 2 * a.pairs;
+    const unsigned items = (unsigned)s.heads * s.row_items;
+    const unsigned per = (items + s.parts - 1) / s.parts;
+    const unsigned i0 = part * per, i1 = min(items, i0 + per);
+    constexpr int kU = 4;
+    bool table = false;
+    for (unsigned base = i0; base < i1 || !table; base += kU * kThreads) {
+        float u[kU][8], v[kU][8];
+        long long at[kU];
+        int pair[kU];  // first pair of a rotated item, -1 for a copied chunk, -2 for none
+#pragma unroll
+        for (int j = 0; j < kU; ++j) {
+            const unsigned i = base + j * kThreads + threadIdx.x;
+            pair[j] = -2;
+            if (i >= i1) continue;
+            const unsigned h = i / (unsigned)s.row_items, c = i % (unsigned)s.row_items;
+            int e;
+            if ((int)c < s.rot) {
+                e = s.off + 8 * c;
+                pair[j] = a.half ? 8 * c : 4 * c;
+            } else {
+                e = 8 * (c - s.rot);
+                if (e >= s.off) e += R;
+                pair[j] = -1;
+            }
+            const T* xp = xt + h * s.xh + e;
+            Vec8<T>::load(xp, u[j]);
+            if (a.half && pair[j] >= 0) Vec8<T>::load(xp + a.pairs, v[j]);
+            at[j] = h * s.oh + e;
+        }
+        if (!table) {  // the first loads are in flight while the angles are worked out
+            block_table(a, b, t, cs);
+            table = true;
+        }
+#pragma unroll
+        for (int j = 0; j < kU; ++j) {
+            if (pair[j] == -2) continue;
+            T* op = ot + at[j];
+            if (pair[j] >= 0 && a.half) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 w = cs[pair[j] + e];
+                    const float x = u[j][e], y = v[j][e];
+                    u[j][e] = x * w.x - y * w.y;
+                    v[j][e] = y * w.x + x * w.y;
+                }
+                Vec8<T>::store(op + a.pairs, v[j]);
+            } else if (pair[j] >= 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 w = cs[pair[j] + e];
+                    const float x = u[j][2 * e], y = u[j][2 * e + 1];
+                    u[j][2 * e] = x * w.x - y * w.y;
+                    u[j][2 * e + 1] = y * w.x + x * w.y;
+                }
+            }
+            Vec8<T>::store(op, u[j]);
+        }
+    }
+    // The attention kernels read their first query before they wait for this grid (they may, once all its
+    // blocks have ended): the rows have reached L2 by then.  For the same reason there is no early
+    // griddep_launch_dependents here.
+    __threadfence();
+}
+
+// any alignment: an item is a pair, or one copied element
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ float2 cs[kMaxPairs];
+    griddep_wait();
+    int part;
+    const RopeStream& s = a.s[which_stream(a, part)];
+    const int b = blockIdx.x / a.n_tok, t = blockIdx.x % a.n_tok;
+    const T* xt = static_cast<const T*>(s.x) + b * s.xb + t * s.xt;
+    T* ot = static_cast<T*>(s.out) + b * s.ob + t * s.ot;
+    block_table(a, b, t, cs);
+    const unsigned items = (unsigned)s.heads * s.row_items;
+    const unsigned per = (items + s.parts - 1) / s.parts;
+    const unsigned i0 = part * per, i1 = min(items, i0 + per);
+    for (unsigned i = i0 + threadIdx.x; i < i1; i += kThreads) {
+        const unsigned h = i / (unsigned)s.row_items, c = i % (unsigned)s.row_items;
+        const T* xp = xt + h * s.xh;
+        T* op = ot + h * s.oh;
+        if ((int)c < s.rot) {
+            const int e0 = s.off + (a.half ? c : 2 * c), e1 = a.half ? e0 + a.pairs : e0 + 1;
+            const float2 w = cs[c];
+            const float x = (float)xp[e0], y = (float)xp[e1];
+            op[e0] = (T)(x * w.x - y * w.y);
+            op[e1] = (T)(y * w.x + x * w.y);
+        } else {
+            int e = c - s.rot;
+            if (e >= s.off) e += 2 * a.pairs;
+            op[e] = xp[e];
+        }
+    }
+    __threadfence();
+}
+
+// whether the rows of out, [n0][n1][n2][d] with these strides, are all apart
+bool rows_apart(long long d, long long n0, long long s0, long long n1, long long s1, long long n2, long long s2) {
+    long long n[3] = {n0, n1, n2}, s[3] = {s0, s1, s2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (s[j] > s[j + 1]) {
+                long long x = s[j]; s[j] = s[j + 1]; s[j + 1] = x;
+                x = n[j]; n[j] = n[j + 1]; n[j + 1] = x;
+            }
+    long long reach = d;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (s[i] < reach) return false;
+        reach += (n[i] - 1) * s[i];
+    }
+    return true;
+}
+
+// turns per position of every pair, each as double + float
+void frequencies(const v4a_rope_params& p, RopeArgs* a) {
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    const long double step = powl((long double)p.base, -2.0L / p.rope_dims);
+    long double f = 1.0L;  // radians
+    for (int k = 0; k < a->pairs; ++k, f *= step) {
+        long double g = f;
+        if (p.orig_ctx > 0) {
+            const long double r = (long double)p.orig_ctx * f / two_pi;
+            long double w = (r - (long double)p.beta_slow) / ((long double)p.beta_fast - (long double)p.beta_slow);
+            w = w < 0 ? 0 : w > 1 ? 1 : w;
+            g = f * w + f / (long double)p.factor * (1 - w);
+        } else {
+            g = f / (long double)p.factor;
+        }
+        g /= two_pi;
+        a->f_hi[k] = (double)g;
+        a->f_lo[k] = (float)(g - (long double)a->f_hi[k]);
+    }
+}
+
+}  // namespace
+}  // namespace v4a
+
+extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, long long n_tok,
+                               const int64_t* positions, long long pos_stride, long long pos0, long long pos_step,
+                               const v4a_rope_params* params, void* stream) {
+    using namespace v4a;
+    if (n_streams < 0 || n_streams > kMaxStreams) return report(V4A_ERR_INVALID_ARG, "v4a_rope: 0 .. 8 streams");
+    if (batch < 0 || n_tok < 0) return report(V4A_ERR_INVALID_ARG, "v4a_rope: need batch >= 0, n_tok >= 0");
+    if (!params) return report(V4A_ERR_INVALID_ARG, "v4a_rope: params is NULL");
+    const v4a_rope_params& p = *params;
+    if (p.rope_dims < 2 || p.rope_dims > 2 * kMaxPairs || (p.rope_dims & 1))
+        return report(V4A_ERR_INVALID_ARG, "v4a_rope: rope_dims must be even and in 2..512");
+    if (!(p.base > 0) || !(p.factor > 0) || !isfinite(p.base) || !isfinite(p.factor) || !isfinite(p.out_scale))
+        return report(V4A_ERR_INVALID_ARG, "v4a_rope: base and factor must be > 0, out_scale finite");
+    if (p.orig_ctx < 0 || (p.orig_ctx > 0 && !(p.beta_fast > p.beta_slow)))
+        return report(V4A_ERR_INVALID_ARG, "v4a_rope: need orig_ctx >= 0 and, with it, beta_fast > beta_slow");
+    if (n_streams == 0 || batch == 0 || n_tok == 0) return V4A_OK;
+    if (!io) return report(V4A_ERR_INVALID_ARG, "v4a_rope: io is NULL");
+    if (n_tok > 0x7fffffffLL || (long long)batch * n_tok > 0x7fffffffLL)
+        return report(V4A_ERR_UNSUPPORTED, "v4a_rope: batch * n_tok must be < 2^31");
+    if (positions && (reinterpret_cast<uintptr_t>(positions) % 8 || pos_stride < 0))
+        return report(V4A_ERR_INVALID_ARG, "v4a_rope: positions misaligned or pos_stride < 0");
+
+    RopeArgs a;
+    bool vec = true;
+    for (int i = 0; i < n_streams; ++i) {
+        v4a_rope_io r = io[i];
+        if (batch == 1) r.x_batch_stride = r.out_batch_stride = 0;  // strides that nothing steps over
+        if (n_tok == 1) r.x_tok_stride = r.out_tok_stride = 0;
+        if (r.heads == 1) r.x_head_stride = r.out_head_stride = 0;
+        if (r.dtype != V4A_F32 && r.dtype != V4A_BF16)
+            return report(V4A_ERR_UNSUPPORTED, "v4a_rope: stream %d: dtype must be F32 or BF16", i);
+        if (r.dtype != io[0].dtype)
+            return report(V4A_ERR_UNSUPPORTED, "v4a_rope: the streams of a call share a dtype");
+        const long long es = r.dtype == V4A_F32 ? 4 : 2;
+        if (!r.x || !r.out || r.heads < 1 || r.d < p.rope_dims || r.rope_offset < 0 ||
+            r.rope_offset > r.d - p.rope_dims || reinterpret_cast<uintptr_t>(r.x) % es ||
+            reinterpret_cast<uintptr_t>(r.out) % es)
+            return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: pointers, heads, d or rope_offset", i);
+        if ((long long)r.heads * r.d > (1LL << 30)) return report(V4A_ERR_UNSUPPORTED, "v4a_rope: stream %d: heads * d too large", i);
+        if (r.x_batch_stride < 0 || r.x_tok_stride < 0 || r.x_head_stride < 0 || r.out_batch_stride < 0 ||
+            r.out_tok_stride < 0 || r.out_head_stride < 0)
+            return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: negative stride", i);
+        if (!rows_apart(r.d, batch, r.out_batch_stride, n_tok, r.out_tok_stride, r.heads, r.out_head_stride))
+            return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: rows of out overlap", i);
+        const bool in_place = r.x == r.out;
+        if (in_place && (r.x_batch_stride != r.out_batch_stride || r.x_tok_stride != r.out_tok_stride ||
+                         r.x_head_stride != r.out_head_stride))
+            return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: in place needs equal strides", i);
+        RopeStream& s = a.s[i];
+        s.x = r.x;
+        s.out = r.out;
+        s.heads = r.heads;
+        s.d = r.d;
+        s.off = r.rope_offset;
+        s.xb = r.x_batch_stride;
+        s.xt = r.x_tok_stride;
+        s.xh = r.x_head_stride;
+        s.ob = r.out_batch_stride;
+        s.ot = r.out_tok_stride;
+        s.oh = r.out_head_stride;
+        s.row_items = in_place ? 0 : r.d - p.rope_dims;  // copied elements; made items below
+        vec = vec && r.d % 8 == 0 && r.rope_offset % 8 == 0 && reinterpret_cast<uintptr_t>(r.x) % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(r.out) % 16 == 0 && (s.xb | s.xt | s.xh | s.ob | s.ot | s.oh) % 8 == 0;
+    }
+    vec = vec && p.rope_dims % (p.half ? 16 : 8) == 0;
+    a.n = n_streams;
+    a.n_tok = (int)n_tok;
+    a.pairs = p.rope_dims / 2;
+    a.half = p.half ? 1 : 0;
+    a.inverse = p.inverse ? 1 : 0;
+    a.scale = (float)p.out_scale;
+    a.positions = positions;
+    a.pos_stride = pos_stride;
+    a.pos0 = pos0;
+    a.pos_step = pos_step;
+    frequencies(p, &a);
+    // Few tokens: cut each token's rows over enough blocks to fill the SMs (one pass of 256 threads x 4 items is
+    // the least worth a block); many tokens: a block per token and stream.
+    const long long tokens = (long long)batch * n_tok;
+    long long want = (8LL * kNumSMs + tokens - 1) / tokens;
+    int blocks_y = 0;
+    for (int i = 0; i < n_streams; ++i) {
+        RopeStream& s = a.s[i];
+        s.rot = vec ? p.rope_dims / (p.half ? 16 : 8) : a.pairs;
+        s.row_items = s.rot + (vec ? s.row_items / 8 : s.row_items);
+        const long long items = (long long)s.heads * s.row_items;
+        const long long most = (items + kThreads - 1) / kThreads;
+        s.parts = (int)(want < most ? want : most);
+        if (s.parts > 65535 / kMaxStreams) s.parts = 65535 / kMaxStreams;
+        blocks_y += s.parts;
+    }
+    const dim3 grid((unsigned)tokens, (unsigned)blocks_y);
+    const bool f32 = io[0].dtype == V4A_F32;
+    auto* kernel = vec ? (f32 ? rope_vec_kernel<float> : rope_vec_kernel<__nv_bfloat16>)
+                       : (f32 ? rope_any_kernel<float> : rope_any_kernel<__nv_bfloat16>);
+    cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? V4A_OK : report(V4A_ERR_CUDA, "v4a_rope: %s", cudaGetErrorString(e));
+}

@@ -403,6 +403,143 @@ V4A_API v4a_status v4a_hca_attend_paged(const void* q, const void* entries, cons
                                         void* stream);
 
 /* ------------------------------------------------------------------ */
+/* serving a batch: rotary positions, shared prefixes, eviction          */
+/* ------------------------------------------------------------------ */
+
+/* One stream of rows to rotate: [batch][n_tok][heads][d] in any order of the
+ * first three dimensions (element strides), the d elements of a row adjacent. */
+typedef struct v4a_rope_io {
+    const void* x;                /* input rows */
+    void* out;                    /* output rows; may be x itself with the same strides (in place: only the
+                                     rotated dims are touched); no other overlap with any x */
+    int heads;                    /* rows per token */
+    int d;                        /* elements per row */
+    int rope_offset;              /* the rotated dims are [rope_offset, rope_offset + rope_dims) */
+    v4a_dtype dtype;              /* F32 or BF16, of x and out */
+    long long x_batch_stride, x_tok_stride, x_head_stride;        /* elements, >= 0 */
+    long long out_batch_stride, out_tok_stride, out_head_stride;  /* elements; rows may not overlap */
+} v4a_rope_io;
+
+typedef struct v4a_rope_params {
+    int rope_dims;      /* R: even, 2 .. 512 */
+    int half;           /* 0: pair k is dims (2k, 2k+1) of the rotated part; 1: dims (k, k + R/2) */
+    int inverse;        /* 0: turn by +angle; 1: by -angle (the gradient of the forward call, and what undoes it
+                           where out_scale is 1) */
+    double base;        /* pair k turns by base^(-2k/R) radians per position, before scaling; > 0 */
+    double factor;      /* context extension s > 0 (1: none) */
+    long long orig_ctx; /* 0: every frequency is divided by s (position interpolation).  > 0: YaRN -- with
+                           r = orig_ctx * f / 2pi turns over the trained length and
+                           g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1), f' = g f + (1 - g) f / s */
+    double beta_fast, beta_slow; /* used when orig_ctx > 0; beta_fast > beta_slow (32 and 1 in YaRN) */
+    double out_scale;   /* the rotated dims are multiplied by this (1: plain; YaRN: 0.1 ln s + 1) */
+} v4a_rope_params;
+
+/* Rotary positions ("1M Context != Lossless Long Memory", section 8: partial
+ * RoPE on the last R = 64 dims; here any part of the row).  For up to 8
+ * streams in one launch -- a decode step's query heads, its new K = V row and
+ * its indexer heads, say -- every pair (a, b) of every row at position p
+ * becomes out_scale * (a cos - b sin, a sin + b cos) of the angle p * f_k;
+ * the row's other dims are copied.  Positions: positions[b * pos_stride + i]
+ * for token i of sequence b (int64, device), or, where positions is NULL,
+ * pos0 + i * pos_step for every sequence (pos_step = m for compressed
+ * entries).  Angles are reduced in more than double precision, so positions
+ * up to 2^40 keep float accuracy.  The attention calls' output rotation
+ * (v4a_attend_ext) is inverse = 1, half = 0 on the last R dims.
+ * Errors: V4A_ERR_INVALID_ARG for NULL pointers, n_streams outside 0..8,
+ * sizes or strides out of range, rows of out that overlap, x = out with
+ * other strides; V4A_ERR_UNSUPPORTED for another dtype. */
+V4A_API v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, long long n_tok,
+                            const int64_t* positions, long long pos_stride, long long pos0, long long pos_step,
+                            const v4a_rope_params* params, void* stream);
+
+/* The cache of a batch whose sequences begin with the same n_prefix entries.
+ * Each sequence has entries of its own behind them, in the first
+ * own_count[b] of own_rows slots, in any state of eviction: slot i holds
+ * entry own_entry[b][i] (a negative one: an empty slot), or entry
+ * n_prefix + i where own_entry is NULL.  The window's tokens come from a ring
+ * as in v4a_paged.  Slots beyond the count, and slots whose entry a query
+ * does not see yet, may hold anything (NaN included). */
+typedef struct v4a_shared_cache {
+    const void* prefix;         /* [n_prefix][d], NULL when n_prefix = 0 */
+    long long n_prefix;
+    const void* own;            /* [batch][own_rows][d], NULL when own_rows = 0 */
+    int own_rows;
+    const int32_t* own_count;   /* [batch], or NULL: own_rows in every sequence */
+    const int32_t* own_entry;   /* [batch][own_rows], or NULL */
+    const void* ring;           /* [batch][ring_rows][d], position p in row p % ring_rows; NULL without a window */
+    int ring_rows;              /* >= window + n_q - 1 */
+    const int64_t* ctx_lens;    /* [batch] tokens of each sequence, or NULL: shape->ctx_len in every one.
+                                   0: a padded sequence, which attends to nothing */
+} v4a_shared_cache;
+
+/* HCA attention over a v4a_shared_cache: v4a_hca_attend_ex for sequences of
+ * different lengths, the prefix read once for the whole batch.  Query j of
+ * sequence b is at position t = ctx_lens[b] - n_q + j; its candidates are the
+ * prefix, the own entries e with m (e + 1) <= t + 1, and the window (t-W, t].
+ * A query before position 0 or not behind the whole prefix
+ * (t + 1 < m * n_prefix) has no candidates; in a sequence of length > 0 the
+ * second is reported as V4A_ERR_DEVICE_FAULT in dev_status (nullable), as are
+ * lengths outside 0 .. shape->ctx_len (taken as 0) and counts outside
+ * 0 .. own_rows (clamped).
+ * out: [batch][n_q][heads][d], out_dtype F32 or (BF16 inputs) BF16; zeros for
+ * a query without candidates.  lse (nullable): [batch][n_q][heads] fp32,
+ * log of the softmax denominator, the sink's share included; -inf for a
+ * query without candidates.  ext: as in the _ex calls, rotated at each
+ * sequence's own positions.  Workspace: v4a_shared_workspace_size bytes,
+ * 256-byte aligned.  Uses shape->batch, n_q, heads, d, m, window, ctx_len.
+ * Errors as v4a_hca_attend, and V4A_ERR_INVALID_ARG for a prefix longer than
+ * ctx_len / m. */
+V4A_API v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, void* out, v4a_dtype out_dtype,
+                                         float* lse, v4a_dtype dtype, void* workspace, size_t workspace_bytes,
+                                         int* dev_status, const v4a_attend_ext* ext, const v4a_shape* shape,
+                                         void* stream);
+/* Bytes of workspace v4a_hca_attend_shared needs (0 for shapes it rejects). */
+V4A_API size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_prefix, int own_rows, v4a_dtype dtype);
+
+/* What every own entry received of the attention, added up over the steps:
+ *     weights_out[b][i] = decay * weights_in[b][i]
+ *                       + sum_{j, h} exp(q[b][j][h] . own[b][i] / sqrt(d) - lse[b][j][h])
+ * for the slots i < own_count[b], the sum running over the queries that see
+ * the slot's entry; a head with lse = -inf (no candidates) adds nothing.  With
+ * the lse of v4a_hca_attend_shared the added terms are that call's softmax
+ * weights.  weights_in / weights_out: [batch][own_rows] fp32, may be the
+ * same; with decay = 0 weights_in is not read and may be NULL.  Slots beyond
+ * the count are left as they were.  The sum's order is fixed: equal inputs give
+ * equal bits.  The cache's prefix and ring are not read (n_prefix, lengths,
+ * counts and entries are).  dev_status as v4a_hca_attend_shared. */
+V4A_API v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, const float* lse,
+                                      const float* weights_in, float* weights_out, float decay, v4a_dtype dtype,
+                                      int* dev_status, const v4a_shape* shape, void* stream);
+
+typedef struct v4a_evict_io {
+    const void* own;            /* [batch][own_rows][d], d * element size a multiple of 16 bytes */
+    const float* weights;       /* [batch][own_rows] */
+    const int32_t* own_count;   /* [batch], or NULL: own_rows */
+    const int32_t* own_entry;   /* [batch][own_rows], or NULL */
+    int own_rows, d;
+    v4a_dtype dtype;            /* F32 or BF16 */
+    void* own_out;              /* [batch][out_rows][d] */
+    float* weights_out;         /* [batch][out_rows] */
+    int32_t* entry_out;         /* [batch][out_rows], or NULL.  Without own_entry: first_entry + slot */
+    int32_t* kept;              /* [batch][budget]: the slots kept, ascending, -1 behind them */
+    int32_t* count_out;         /* [batch] */
+    int out_rows;               /* >= budget */
+    int first_entry;            /* the entry that slot 0 holds where own_entry is NULL (n_prefix) */
+} v4a_evict_io;
+
+/* Eviction by accumulated attention weight: of each sequence's
+ * n = own_count[b] slots keep min(budget, n) -- the first keep_first and the
+ * last keep_recent, then those with the largest weights, ties going to the
+ * lower slot and NaN weights last -- and move them, in order, to the front of
+ * own_out, weights_out and entry_out.  Output rows behind the kept ones are
+ * left as they were.  Inputs and outputs may not overlap.
+ * dev_status (nullable): V4A_ERR_DEVICE_FAULT for a count outside
+ * 0 .. own_rows (clamped).  Errors: V4A_ERR_INVALID_ARG for NULL or misaligned
+ * pointers, budget < 1, keep_first + keep_recent > budget, overlap. */
+V4A_API v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, int keep_first, int keep_recent,
+                             int* dev_status, void* stream);
+
+/* ------------------------------------------------------------------ */
 /* housekeeping                                                         */
 /* ------------------------------------------------------------------ */
 
