@@ -459,6 +459,7 @@ v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, v
         const cudaError_t e = launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, s);
         if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
     }
+    if (shared_tc_shape_ok(a)) return from_cuda(launch_shared_tc(a, workspace, s), what);
     return from_cuda(by_shape(a, [&](auto t, auto d) { return simt_attend<decltype(t), decltype(d)::value>(a, workspace, s); }), what);
 }
 
@@ -476,7 +477,7 @@ size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_prefix, int
     a.own_rows = own_rows;
     a.n_prefix = n_prefix;
     a.dtype = dtype;
-    return simt_bytes(a);
+    return shared_tc_shape_ok(a) ? shared_tc_workspace_bytes(a) : simt_bytes(a);
 }
 
 v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, const float* lse, const float* weights_in,

@@ -1,0 +1,790 @@
+// attend_shared_tc.cu -- tensor-core (tcgen05 / TMEM / TMA) HCA attention over a prefix that a batch shares
+// (bf16, d = 512, any number of heads).
+//
+//     out = sum_r p_r v_r,  p = softmax_r(q . v_r / sqrt(d)),  lse = log sum_r e^{q . v_r / sqrt(d)}
+//
+// Every query of the batch sees the whole prefix, so the rows (sequence, query, head) of all sequences are
+// one matrix, taken in groups of 128 that ignore where a sequence ends.  A group's keys are tiles of 64:
+// the prefix, then the own slots and the window of each sequence that has rows in the group; rows of
+// other sequences are masked there.  The tiles of all groups form one flat sequence, cut into equal ranges.
+//
+// A range goes to a CTA pair (two SMs, cta_group::2), each CTA holding 64 of the 128 rows.  Per tile
+//     S  = Q K^T   M = 128 rows x N = 64 keys x K = 512    (each CTA brings 32 of the keys)
+//     P  = softmax(S), two threads per row, lazily rescaled maximum
+//     O += P V     M = 128 x N = 2 x 256 dims x K = 64 keys (each CTA brings half of the dims)
+// With 64 rows of 512 dims a CTA's O is half of tensor memory, and 64 rows at the full rate of the tensor
+// cores need the pair: alone a CTA runs M = 64 at half rate.  Since S wants all dims of half of the keys and
+// O half of the dims of all keys, a stage of 32 KB is used twice: it is loaded with this CTA's 32 keys
+// ("X"), and once S is done the slabs of dims that O does not need here make room for the other 32 keys
+// of those that it does ("Z").  So a tile costs 48 KB of loads per CTA and 32 KB of shared memory, and
+// four stages fit beside the 64 KB of queries.
+//
+// Slabs are 64 dims (128 bytes) wide; slab s of the CTA's own keys lies at 4096 s.  CTA 0 has the even slabs
+// of O, CTA 1 the odd ones: block u (8192 u) becomes the 64 keys of slab 2 u + rank.
+//
+// Masked places may hold anything.  A NaN or infinity in a row of K = V makes the raw S of every row of the
+// matrix non-finite at that key, so the softmax threads see it, also for rows that do not see the
+// key; such a tile's V is scrubbed of non-finite values before the product (0 x NaN would spoil the rows of
+// other sequences).  Rows that do see the key have a NaN in P, or weight 0 for a logit of -inf.
+//
+// Warps: 0 loads Q and X, 6 loads Z, 1 (of CTA 0) issues the MMAs, 2-5 run the softmax and write pieces.
+// Every wait is bounded; on a time-out both CTAs record a device fault, their pieces become NaN and they
+// wind down.  Pieces (m, l, O) are merged by shared_tc_join_kernel: out = sum_i e^{m_i - m} o_i / l.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "shared.h"
+#include "tc.cuh"
+
+namespace v4a {
+namespace {
+
+constexpr int kD = 512;
+constexpr int kRows = 128;          // rows of a group
+constexpr int kHalf = 64;           // ... of one CTA
+constexpr int kKeys = 64;           // keys of a tile
+constexpr int kStages = 4;
+constexpr int kSBufs = 3;
+constexpr int kPairs = kNumSMs / 2;
+constexpr uint32_t kXBytes = 32 * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
+constexpr uint32_t kColS = 256, kColsS = 32, kTmemCols = 512;  // O: columns 0-255
+constexpr int kThreads = 7 * 32;
+constexpr long long kStall = 1LL << 31;  // cycles without progress after which the MMA warp gives up
+constexpr float kSlack = 8.0f;           // keep a stale running max until the true one exceeds it by 2^8
+constexpr uint32_t kIdescQK = tc::idesc_f16(128, kKeys, 0, 0), kIdescPV = tc::idesc_f16(128, 256, 0, 1);
+
+struct __align__(1024) Smem {
+    uint8_t q[kQBytes];
+    uint8_t kv[kStages][kXBytes];
+    uint8_t p[2][kHalf * 128];
+    float mx[2][4][32];  // row maxima of a tile's halves, by tile parity
+    float ls[4][32];
+    // x_full, z_ready, p_full and q_full count in CTA 0 only
+    uint64_t x_full[kStages], z_full[kStages], z_ready[kStages], kv_empty[kStages], s_full[kSBufs], p_full[2], p_free[2];
+    uint64_t q_full, q_empty, drain;
+    int abort_flag;
+    uint32_t tmem_base;
+};
+
+struct PairArgs {
+    SharedArgs a;
+    float2* part_ml;       // [pieces][128] (m in base-2 logits, l)
+    float4* part_o;        // [pieces][128 quads of dims][128 rows]
+    long long total;       // tiles of all groups
+    unsigned rows, per_seq, lcm;  // batch * n_q * heads; n_q * heads; least common multiple of that and 128
+    int groups, pairs;
+    int pre, own, win;     // tiles: prefix; own and window of a sequence (win: one more than the window fills, for a
+                           // ring that wraps inside it)
+    float scale_log2;
+    int g0[kPairs + 1];    // group of every pair's first tile
+};
+
+// tiles of the groups before g.  A group has `pre` tiles and own + win for every sequence with rows in it: one
+// more than the sequences that begin inside it, behind its first row.
+__host__ __device__ inline long long tiles_before(const PairArgs& c, int g) {
+    if (g == 0) return 0;
+    const unsigned long long e = (unsigned long long)g * kRows;
+    const unsigned last = (unsigned)(e < c.rows ? e : c.rows) - 1;
+    const long long seqs = g + (long long)(last / c.per_seq) - (long long)(last / c.lcm);
+    return (long long)g * c.pre + seqs * (c.own + c.win);
+}
+__device__ __forceinline__ long long range_start(const PairArgs& c, int pair) { return (long long)pair * c.total / c.pairs; }
+
+enum Kind { kPrefix, kOwn, kWindow };
+
+struct Tile {
+    int group, kind, b;  // b: the sequence (own, window)
+    int y, n;            // first row of its 64 in prefix / own / ring, rows that count
+    long long p0;        // what row y holds: own slot, or position
+    bool first;          // first tile of its piece
+};
+
+// walks the tiles of a range that hold anything, the same in every role
+struct Walk {
+    long long left;
+    int g, i, per, seq0, seqs;  // group, tile in it, its tiles, its sequences
+    int s, w;                   // sequence and its tile
+    bool fresh;
+    int count, row0, n_a, n_w;  // own slots; window: ring row of position lo, positions before the ring's end, all
+    long long lo;
+
+    __device__ void enter_group(const PairArgs& c) {
+        const unsigned r0 = (unsigned)g * kRows, r1 = min(r0 + kRows, c.rows) - 1;
+        seq0 = (int)(r0 / c.per_seq);
+        seqs = (int)(r1 / c.per_seq) - seq0 + 1;
+        per = c.pre + seqs * (c.own + c.win);
+        fresh = true;
+        s = seq0;
+        w = 0;
+    }
+    __device__ void enter_sequence(const PairArgs& c) {
+        const long long len = seq_len(c.a, s);
+        count = len > 0 ? own_slots(c.a, s) : 0;
+        lo = len - c.a.n_q - c.a.window + 1;
+        lo = lo < 0 ? 0 : lo;
+        n_w = c.a.window > 0 && len > 0 ? (int)(len - lo) : 0;
+        row0 = n_w > 0 ? (int)(lo % c.a.ring_rows) : 0;
+        n_a = n_w < c.a.ring_rows - row0 ? n_w : c.a.ring_rows - row0;
+    }
+    __device__ Walk(const PairArgs& c, int pair) {
+        const long long f0 = range_start(c, pair);
+        left = range_start(c, pair + 1) - f0;
+        g = c.g0[pair];
+        i = (int)(f0 - tiles_before(c, g));
+        enter_group(c);
+        if (i >= c.pre && left > 0) {
+            const int k = i - c.pre;
+            s = seq0 + k / (c.own + c.win);
+            w = k % (c.own + c.win);
+            enter_sequence(c);
+        }
+    }
+    __device__ bool next(const PairArgs& c, Tile& t) {
+        while (left > 0) {
+            if (i == per) {
+                ++g;
+                i = 0;
+                enter_group(c);
+                if (c.pre == 0) enter_sequence(c);
+            }
+            --left;
+            bool live = true;
+            if (i < c.pre) {
+                t.kind = kPrefix;
+                t.y = i * kKeys;
+                const long long n = c.a.n_prefix - t.y;
+                t.n = n < kKeys ? (int)n : kKeys;
+                t.b = 0;
+                t.p0 = t.y;
+                if (++i == c.pre && i < per) enter_sequence(c);
+            } else {
+                t.b = s;
+                if (w < c.own) {
+                    t.kind = kOwn;
+                    t.y = w * kKeys;
+                    t.p0 = t.y;
+                    t.n = min(count - t.y, kKeys);
+                } else {
+                    int at = (w - c.own) * kKeys;
+                    const int a_rows = (n_a + kKeys - 1) / kKeys * kKeys;
+                    t.kind = kWindow;
+                    if (at < a_rows) {
+                        t.y = row0 + at;
+                        t.p0 = lo + at;
+                        t.n = min(n_a - at, kKeys);
+                    } else {
+                        at -= a_rows;
+                        t.y = at;
+                        t.p0 = lo + n_a + at;
+                        t.n = min(n_w - n_a - at, kKeys);
+                    }
+                }
+                live = t.n > 0;
+                ++i;
+                if (++w == c.own + c.win) {
+                    w = 0;
+                    ++s;
+                    if (i < per) enter_sequence(c);
+                }
+            }
+            if (live) {
+                t.group = g;
+                t.first = fresh;
+                fresh = false;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+__device__ void fault(Smem& sm, const PairArgs& c, uint32_t rank) {
+    *reinterpret_cast<volatile int*>(&sm.abort_flag) = 1;
+    tc::peer_store(tc::peer_addr(&sm.abort_flag, rank ^ 1), 1);
+    if (c.a.dev_status) atomicExch(c.a.dev_status, (int)V4A_ERR_DEVICE_FAULT);
+}
+__device__ __forceinline__ bool aborted(Smem& sm) { return *reinterpret_cast<volatile int*>(&sm.abort_flag) != 0; }
+
+// ---------------------------------------------------------------------
+// warp 0, one lane: queries and this CTA's 32 keys of every tile.  Both CTAs' copies complete on CTA 0's
+// barriers, which expect the bytes of both.
+// ---------------------------------------------------------------------
+struct Maps {
+    CUtensorMap x[3], z[3], q;  // by Kind: 32 rows x 8 slabs; 32 rows x 1 slab
+};
+
+__device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
+    const uint64_t again = tc::l2_evict_normal(), once = tc::l2_stream_policy((int)((c.per_seq + kRows - 1) / kRows));
+    Walk walk(c, pair);
+    Tile t;
+    int j = 0, piece = 0;
+    bool ok = true;
+    while (walk.next(c, t)) {
+        if (aborted(sm)) { ok = false; break; }
+        if (t.first) {
+            if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1)) { ok = false; break; }
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
+            tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, tc::peer_addr(&sm.q_full, 0), again);
+            ++piece;
+        }
+        const int st = j % kStages;
+        if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st], (j / kStages - 1) & 1)) { ok = false; break; }
+        if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
+        tc::tma_load_4d_pair(sm.kv[st], &maps.x[t.kind], 0, t.y + (int)rank * 32, 0, t.b, tc::peer_addr(&sm.x_full[st], 0),
+                             t.kind == kPrefix ? again : once);
+        ++j;
+    }
+    if (!ok) {  // what was asked for lands long before this ends
+        fault(sm, c, rank);
+        for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+    }
+}
+
+// warp 6, one lane: the other CTA's 32 keys of this CTA's slabs, once S has been computed
+__device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
+    const uint64_t again = tc::l2_evict_normal();
+    Walk walk(c, pair);
+    Tile t;
+    int j = 0;
+    bool ok = true, more = true;
+    for (;; ++j) {
+        more = ok && !aborted(sm) && walk.next(c, t);
+        if (more && !tc::mbar_wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) ok = more = false;
+        if (more) {
+            const int st = j % kStages;
+            const uint32_t other = rank ^ 1;
+            tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u)
+                tc::tma_load_4d(sm.kv[st] + 8192 * u + 4096 * other, &maps.z[t.kind], 0, t.y + (int)other * 32, 2 * u + (int)rank,
+                                t.b, &sm.z_full[st], again);
+        }
+        if (j > 0) {  // the tile before has landed meanwhile
+            const int st = (j - 1) % kStages;
+            if (!tc::mbar_wait(&sm.z_full[st], ((j - 1) / kStages) & 1)) ok = false;
+            else {
+                tc::fence_proxy_async();
+                tc::peer_arrive(tc::peer_addr(&sm.z_ready[st], 0));
+            }
+        }
+        if (!more) break;
+    }
+    if (!ok) fault(sm, c, rank);
+}
+
+// ---------------------------------------------------------------------
+// warp 1 of CTA 0: every MMA of the pair, in whatever order its inputs become ready
+// ---------------------------------------------------------------------
+__device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+__device__ void issue(Smem& sm, const PairArgs& c, uint32_t tmem, int pair) {
+    Walk walk(c, pair);
+    Tile t, nxt;
+    bool more = walk.next(c, t), ok = true;
+    int jq = 0, jp = 0, pieces = 0;
+    uint32_t firsts = 0;  // by tile modulo 32: first of its piece
+    const uint64_t q0 = tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024);
+    long long t_last = clock64();
+    while (more || jp < jq) {
+        if (__shfl_sync(0xffffffffu, (int)aborted(sm), 0)) { ok = false; break; }
+        bool progressed = false;
+        if (jp < jq && tc::mbar_test_warp_cluster(&sm.p_full[jp & 1], (uint32_t)(jp >> 1) & 1) &&
+            tc::mbar_test_warp_cluster(&sm.z_ready[jp % kStages], (uint32_t)(jp / kStages) & 1)) {
+            tc::tc_fence_after();
+            const int st = jp % kStages;
+            // A = P (64 rows of 128 bytes per CTA); B = V, 16 keys x 128 dims (2 slabs, 8 KB apart) per CTA
+            const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.p[jp & 1]), 16, 1024);
+            const uint64_t b0 = tc::sw128_desc(tc::smem_u32(sm.kv[st]), 8192, 1024);
+            const bool first = (firsts >> (jp & 31)) & 1;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    tc::mma_f16_pair(tmem + 128 * h, dadd(a0, kk * 32), dadd(b0, 16384 * h + kk * 2048), kIdescPV,
+                                     (!first || kk > 0) ? 1u : 0u);
+            tc::mma_commit_pair(&sm.kv_empty[st]);
+            tc::mma_commit_pair(&sm.p_free[jp & 1]);
+            ++jp;
+            progressed = true;
+        } else if (more && jq - jp < kSBufs && tc::mbar_test_warp_cluster(&sm.x_full[jq % kStages], (uint32_t)(jq / kStages) & 1) &&
+                   (!t.first || tc::mbar_test_warp_cluster(&sm.q_full, pieces & 1))) {
+            tc::tc_fence_after();
+            const uint64_t k0 = tc::sw128_desc(tc::smem_u32(sm.kv[jq % kStages]), 16, 1024);
+            const uint32_t d_s = tmem + kColS + kColsS * (jq % kSBufs);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_f16_pair(d_s, dadd(q0, s * 8192 + kk * 32), dadd(k0, s * 4096 + kk * 32), kIdescQK,
+                                     (s | kk) ? 1u : 0u);
+            tc::mma_commit_pair(&sm.s_full[jq % kSBufs]);
+            firsts = (firsts & ~(1u << (jq & 31))) | ((uint32_t)t.first << (jq & 31));
+            pieces += t.first;
+            more = walk.next(c, nxt);
+            if (!more || nxt.first) tc::mma_commit_pair(&sm.q_empty);  // the last S of this piece
+            t = nxt;
+            ++jq;
+            progressed = true;
+        }
+        if (progressed) {
+            t_last = clock64();
+        } else if (__shfl_sync(0xffffffffu, (int)(clock64() - t_last > kStall), 0)) {
+            ok = false;
+            break;
+        }
+    }
+    if (!ok) fault(sm, c, 0);
+    tc::mma_commit_pair(&sm.drain);
+}
+
+// ---------------------------------------------------------------------
+// warps 2-5: softmax, rescaling, pieces
+// ---------------------------------------------------------------------
+__device__ __forceinline__ uint32_t low_bits(long long n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// zero what is not finite in 8 bf16
+__device__ __forceinline__ uint32_t scrub(uint32_t x) {
+    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+    return x;
+}
+
+__device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, uint32_t rank) {
+    const SharedArgs& a = c.a;
+    const int sub = (threadIdx.x >> 5) & 3;  // TMEM lanes 32 sub ..: rows 32 (sub & 1) .., keys or dims of half sub >> 1
+    const int lane = threadIdx.x & 31, half = sub >> 1, r = 32 * (sub & 1) + lane;
+    const int bar = 1 + (sub & 1);  // the two warps that share rows
+    const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
+    const uint32_t p_full[2] = {tc::peer_addr(&sm.p_full[0], 0), tc::peer_addr(&sm.p_full[1], 0)};
+    Walk walk(c, pair);
+    Tile t, nxt;
+    bool more = walk.next(c, t), ok = true;
+    int next_group = c.g0[pair];
+    float m_run = -INFINITY, l_run = 0.f;
+    // this row's query
+    int b = 0;
+    long long pos = 0, seen = 0;
+    bool alive = false;
+    auto wait = [&](uint64_t* bar_, uint32_t parity) {
+        if (ok && (aborted(sm) || !tc::mbar_wait(bar_, parity))) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+    };
+    // a time-out leaves `ok` false: the rest of the range is walked for its barriers only
+    for (int j = 0; more; ++j) {
+        if (t.first) {
+            m_run = -INFINITY;
+            l_run = 0.f;
+            const unsigned row = (unsigned)t.group * kRows + rank * kHalf + r;
+            alive = row < c.rows;
+            if (alive) {
+                const unsigned query = row / (unsigned)a.heads;
+                b = (int)(query / (unsigned)a.n_q);
+                pos = seq_len(a, b) - a.n_q + (int)(query % (unsigned)a.n_q);
+                alive = has_candidates(a, pos);
+                seen = seen_entries(a, pos);
+            }
+        }
+        // this thread's 32 keys
+        uint32_t mask = 0;
+        const int n = t.n - 32 * half;
+        if (t.kind == kPrefix) {
+            mask = alive ? low_bits(n) : 0u;
+        } else if (t.kind == kOwn) {
+            const bool mine = alive && b == t.b;
+            if (a.own_entry) {
+                int e = -1;
+                if (lane < n) e = a.own_entry[(long long)t.b * a.own_rows + t.p0 + 32 * half + lane];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const int ek = __shfl_sync(0xffffffffu, e, k);
+                    mask |= (uint32_t)(ek >= 0 && ek < seen) << k;
+                }
+                if (!mine) mask = 0;
+            } else if (mine) {
+                const long long lim = seen - a.n_prefix - t.p0 - 32 * half;
+                mask = low_bits(lim < n ? lim : n);
+            }
+        } else if (alive && b == t.b) {
+            const long long from = pos - a.window + 1 - t.p0 - 32 * half, to = pos + 1 - t.p0 - 32 * half;
+            mask = low_bits(to < n ? to : n) & ~low_bits(from);
+        }
+        float x[32];
+        if (wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) {
+            tc::tc_fence_after();
+            uint32_t u[32];
+            tc::tmem_ld_x32(lanes + kColS + kColsS * (j % kSBufs), u);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(u[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = 0.f;
+        }
+        bool odd = false;  // a key of this tile is not finite
+        if (t.kind != kPrefix) {
+            float d = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) d = fmaf(x[k], 0.f, d);
+            odd = !(d == 0.f);
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (mask == ~0u) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                x[k] = (mask >> k) & 1 ? x[k] : -INFINITY;
+                mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
+            }
+        }
+        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c.scale_log2;
+        sm.mx[j & 1][sub][lane] = mt;
+        if (t.kind == kPrefix) tc::named_barrier(bar, 64);
+        else odd = tc::named_barrier_or(3, 128, odd);
+        mt = fmaxf(mt, sm.mx[j & 1][sub ^ 2][lane]);
+        float alpha = 1.f;
+        if (mt > m_run + kSlack) {
+            if (m_run != -INFINITY) alpha = exp2f(m_run - mt);
+            m_run = mt;
+        }
+        l_run *= alpha;
+        const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
+        uint32_t pk[16];
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float p0 = exp2f(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2f(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
+            ls[k & 3] += p0 + p1;  // the sum is of the unrounded weights
+            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+            pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+        }
+        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
+        if (rescale && wait(&sm.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {  // O is complete up to the tile before
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[64];
+                tc::tmem_ld_x64(lanes + 64 * q, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tc::tmem_st_x64(lanes + 64 * q, o);
+            }
+            tc::tmem_st_wait();
+        }
+        // the P buffer of this parity is free once the product two tiles back is done
+        if (j < 2 || wait(&sm.p_free[j & 1], ((j >> 1) - 1) & 1)) {
+            uint8_t* prow = sm.p[j & 1] + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(prow + (((4 * half + k) ^ (r & 7)) << 4)) =
+                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        }
+        if (odd && wait(&sm.z_full[j % kStages], (j / kStages) & 1)) {
+            // both halves of V are here: scrub it, a row of 128 bytes at a time
+            uint4* v = reinterpret_cast<uint4*>(sm.kv[j % kStages]);
+            for (int k = threadIdx.x - 64; k < (int)(kXBytes / 16); k += 128) {
+                const uint4 w = v[k];
+                v[k] = make_uint4(scrub(w.x), scrub(w.y), scrub(w.z), scrub(w.w));
+            }
+        }
+        tc::fence_proxy_async();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) tc::peer_arrive(p_full[j & 1]);
+
+        more = walk.next(c, nxt);
+        if (!more || nxt.first) {
+            // write the piece
+            const long long piece = pair + t.group;
+            for (; next_group < t.group; ++next_group)  // groups of the range without a tile that holds anything
+                if (half == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
+            next_group = t.group + 1;
+            sm.ls[sub][lane] = l_run;
+            tc::named_barrier(bar, 64);
+            if (half == 0) {
+                const float l = l_run + sm.ls[sub ^ 2][lane];
+                c.part_ml[piece * kRows + rank * kHalf + r] = make_float2(isnan(l) ? NAN : m_run, l);
+            }
+            if (wait(&sm.p_free[j & 1], (j >> 1) & 1)) {
+                tc::tc_fence_after();
+                float4* po = c.part_o + piece * (kRows * kD / 4) + rank * kHalf + r;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[64];
+                    tc::tmem_ld_x64(lanes + 64 * q, o);
+                    tc::tmem_ld_wait();
+                    float4* pq = po + (long long)(2 * q + half) * 16 * kRows;  // slab 2 q + half
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        pq[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                    __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                }
+                tc::tc_fence_before();
+            }
+        }
+        t = nxt;
+    }
+    const long long f1 = range_start(c, pair + 1);
+    for (; next_group < c.groups && tiles_before(c, next_group) < f1; ++next_group)
+        if (half == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
+    if (!ok || aborted(sm)) {
+        fault(sm, c, rank);
+        for (int g = c.g0[pair]; g < next_group; ++g)
+            if (half == 0) c.part_ml[(pair + (long long)g) * kRows + rank * kHalf + r] = make_float2(NAN, NAN);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs c) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&sm.x_full[i], 1);
+            tc::mbar_init(&sm.z_full[i], 1);
+            tc::mbar_init(&sm.z_ready[i], 2);
+            tc::mbar_init(&sm.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kSBufs; ++i) tc::mbar_init(&sm.s_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.p_full[i], 8);  // the softmax warps of both CTAs
+            tc::mbar_init(&sm.p_free[i], 1);
+        }
+        tc::mbar_init(&sm.q_full, 1);
+        tc::mbar_init(&sm.q_empty, 1);
+        tc::mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) tc::tmem_alloc_pair(&sm.tmem_base, kTmemCols);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    griddep_wait();  // everything before this kernel on the stream has finished
+    const uint32_t tmem = sm.tmem_base;
+    if (warp == 0) {
+        if (lane == 0) load_x(sm, c, maps, pair, rank);
+    } else if (warp == 6) {
+        if (lane == 0) load_z(sm, c, maps, pair, rank);
+    } else if (warp == 1) {
+        if (rank == 0) issue(sm, c, tmem, pair);
+    } else {
+        softmax(sm, c, tmem, pair, rank);
+    }
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // neither CTA leaves, or frees tensor memory, while the other uses it
+    if (warp == 1) {
+        tc::mbar_wait(&sm.drain, 0);  // every MMA issued has completed
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// Joins the pieces.  A block takes 32 rows (a lane each) and 16 dims (4 per warp): a warp's load of a
+// piece is 512 contiguous bytes.  The output leaves through shared memory, 32 or 64 bytes per row.
+__global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_constant__ PairArgs c) {
+    griddep_wait();
+    griddep_launch_dependents();
+    __shared__ float tile[32][20];
+    const SharedArgs& a = c.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned row = blockIdx.x * 32 + lane;
+    const int g = (int)(blockIdx.x / (kRows / 32)), rg = (int)(row % kRows);
+    const int quad = blockIdx.y * 4 + warp, dim = quad * 4;
+    bool live = false;
+    long long pos = 0;
+    int h = 0;
+    if (row < c.rows) {
+        const unsigned query = row / (unsigned)a.heads;
+        h = (int)(row % (unsigned)a.heads);
+        const int b = (int)(query / (unsigned)a.n_q);
+        pos = seq_len(a, b) - a.n_q + (int)(query % (unsigned)a.n_q);
+        live = has_candidates(a, pos);
+        if (blockIdx.y == 0 && warp == 0 && h == 0 && query % (unsigned)a.n_q == 0) report_sequence(a, b);
+    }
+    // pieces of this group: pairs p0 .. p0 + n - 1
+    int p0 = 0, n = 0;
+    if (c.total > 0) {
+        const long long f0 = tiles_before(c, g), f1 = tiles_before(c, g + 1);
+        p0 = (int)(((f0 + 1) * c.pairs - 1) / c.total);
+        n = (int)((f1 * c.pairs - 1) / c.total) - p0 + 1;
+    }
+    const float2* ml = c.part_ml + (long long)(p0 + g) * kRows + rg;
+    const float4* po = c.part_o + (long long)(p0 + g) * (kRows * kD / 4) + quad * kRows + rg;
+    float m = -INFINITY;
+    if (live)
+        for (int i = 0; i < n; ++i) {
+            const float x = ml[(long long)i * kRows].x;
+            m = isnan(x) || isnan(m) ? NAN : fmaxf(m, x);
+        }
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m != -INFINITY) {
+        constexpr int kU = 4;  // pieces in flight
+        for (int i0 = 0; i0 < n; i0 += kU) {
+            float4 v[kU];
+            float2 x[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (i0 + u >= n) continue;
+                x[u] = ml[(long long)(i0 + u) * kRows];
+                if (x[u].x != -INFINITY) v[u] = __ldcg(po + (long long)(i0 + u) * (kRows * kD / 4));  // else: never written
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (i0 + u >= n || x[u].x == -INFINITY) continue;
+                const float w = exp2f(x[u].x - m);
+                l = fmaf(w, x[u].y, l);
+                o.x = fmaf(w, v[u].x, o.x);
+                o.y = fmaf(w, v[u].y, o.y);
+                o.z = fmaf(w, v[u].z, o.z);
+                o.w = fmaf(w, v[u].w, o.w);
+            }
+        }
+        if (a.sink) l += exp2f(a.sink[h] * kLog2eF - m);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+    if (a.lse && blockIdx.y == 0 && warp == 0 && row < c.rows)
+        a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
+    o.x *= inv;
+    o.y *= inv;
+    o.z *= inv;
+    o.w *= inv;
+    const int r0 = kD - a.rope_dims;
+    if (a.rope_dims > 0 && live) {
+        float s, co;
+        if (dim >= r0) {
+            rope_sincos(pos, (dim - r0) >> 1, a.rope_dims, a.rope_base, &s, &co);
+            const float u = o.x;
+            o.x = fmaf(u, co, -o.y * s);
+            o.y = fmaf(u, s, o.y * co);
+        }
+        if (dim + 2 >= r0) {
+            rope_sincos(pos, (dim + 2 - r0) >> 1, a.rope_dims, a.rope_base, &s, &co);
+            const float u = o.z;
+            o.z = fmaf(u, co, -o.w * s);
+            o.w = fmaf(u, s, o.w * co);
+        }
+    }
+    *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = o;
+    __syncthreads();
+    const int tr = threadIdx.x >> 2, part = threadIdx.x & 3;  // 4 threads per row
+    const long long orow = (long long)blockIdx.x * 32 + tr;
+    if (orow >= c.rows) return;
+    const float4 v = *reinterpret_cast<const float4*>(&tile[tr][4 * part]);
+    const long long at = orow * kD + blockIdx.y * 16 + 4 * part;
+    if (a.out_dtype == V4A_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+    } else {
+        const __nv_bfloat162 p[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = *reinterpret_cast<const uint2*>(p);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// [n][rows][512] bf16 viewed as (64 columns, rows, 8 slabs, n); a box is box_rows rows of `slabs` slabs
+bool make_map(CUtensorMap* map, const void* base, long long n, long long rows, int box_rows, int slabs) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)rows, 8, (cuuint64_t)n};
+    cuuint64_t strides[3] = {kD * 2, 128, (cuuint64_t)rows * kD * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)slabs, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// everything of the arguments that the sizes alone decide
+void plan(const SharedArgs& a, PairArgs* c) {
+    c->a = a;
+    c->rows = (unsigned)((long long)a.batch * a.n_q * a.heads);
+    c->per_seq = (unsigned)(a.n_q * a.heads);
+    unsigned x = c->per_seq, y = kRows;
+    while (y) { const unsigned z = x % y; x = y; y = z; }
+    const unsigned long long lcm = (unsigned long long)(c->per_seq / x) * kRows;
+    c->lcm = lcm < 0xffffffffULL ? (unsigned)lcm : 0xffffffffu;  // beyond every row: divides to 0 either way
+    c->groups = (int)((c->rows + kRows - 1) / kRows);
+    c->pre = (int)((a.n_prefix + kKeys - 1) / kKeys);
+    c->own = (a.own_rows + kKeys - 1) / kKeys;
+    c->win = a.window > 0 ? (int)(((long long)a.window + a.n_q - 1 + kKeys - 1) / kKeys) + 1 : 0;
+    c->total = tiles_before(*c, c->groups);
+    c->pairs = c->total < kPairs ? (int)c->total : kPairs;
+    c->scale_log2 = kLog2eF / sqrtf((float)kD);
+    int g = 0;
+    for (int p = 0; p < c->pairs; ++p) {
+        const long long f = (long long)p * c->total / c->pairs;
+        int hi = c->groups;  // the last group that begins at or before tile f
+        while (hi - g > 1) {
+            const int mid = g + (hi - g) / 2;
+            if (tiles_before(*c, mid) <= f) g = mid;
+            else hi = mid;
+        }
+        c->g0[p] = g;
+    }
+}
+long long pieces(const PairArgs& c) { return c.total > 0 ? (long long)c.groups + c.pairs - 1 : 0; }
+
+}  // namespace
+
+bool shared_tc_shape_ok(const SharedArgs& a) {
+    return a.dtype == V4A_BF16 && a.d == kD &&
+           (long long)a.n_prefix + (long long)a.batch * ((long long)a.own_rows + a.window + a.n_q) < (1LL << 31);
+}
+
+size_t shared_tc_workspace_bytes(const SharedArgs& a) {
+    PairArgs c;
+    plan(a, &c);
+    return align256(pieces(c) * kRows * sizeof(float2)) + pieces(c) * kRows * kD * sizeof(float);
+}
+
+cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
+    PairArgs c;
+    plan(a, &c);
+    c.part_ml = static_cast<float2*>(ws);
+    c.part_o = reinterpret_cast<float4*>(static_cast<char*>(ws) + align256(pieces(c) * kRows * sizeof(float2)));
+    Maps maps;
+    if (c.total > 0) {
+        const struct { const void* p; long long n, rows; } in[3] = {
+            {a.prefix, 1, a.n_prefix}, {a.own, a.batch, a.own_rows}, {a.window > 0 ? a.ring : nullptr, a.batch, a.ring_rows}};
+        bool ok = make_map(&maps.q, a.q, 1, c.rows, kHalf, 8);
+        for (int k = 0; k < 3; ++k) {
+            const bool have = in[k].p && in[k].rows > 0;  // without: no tile asks for it
+            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, 32, 8) &&
+                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, 32, 1);
+        }
+        if (!ok) return cudaErrorNotSupported;
+        const size_t smem = sizeof(Smem) + 1024;
+        static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
+        cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = launch_pdl_cluster(shared_tc_kernel, dim3(2 * c.pairs), dim3(kThreads), smem, st, 2, maps, c);
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = launch_pdl(shared_tc_join_kernel, dim3((c.rows + 31) / 32, kD / 16), dim3(128), 0, st, c);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace v4a

@@ -73,4 +73,9 @@ __device__ __forceinline__ void report_sequence(const SharedArgs& a, int b) {
     if (bad) atomicExch(a.dev_status, (int)V4A_ERR_DEVICE_FAULT);
 }
 
+// ---- attend_shared_tc.cu (tcgen05 path: bf16, d = 512) ------------------
+bool shared_tc_shape_ok(const SharedArgs& a);
+size_t shared_tc_workspace_bytes(const SharedArgs& a);
+cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t stream);
+
 }  // namespace v4a
