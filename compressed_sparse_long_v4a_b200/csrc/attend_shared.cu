@@ -504,6 +504,7 @@ v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, cons
         if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
     }
     if (a.own_rows == 0) return V4A_OK;
+    if (weights_tc_shape_ok(a)) return from_cuda(launch_weights_tc(a, s), what);
     return from_cuda(by_shape(a, [&](auto t, auto d) { return simt_weights<decltype(t), decltype(d)::value>(a, s); }), what);
 }
 
