@@ -3,7 +3,9 @@
 The functions here carry the C ABI's names (``include/v4a.h``) and only
 marshal arguments: they read pointers, sizes and strides off torch tensors,
 pass the current CUDA stream, and raise ``V4AError`` with the library's
-one-line reason when a call returns a non-OK status.  Every step of the
+one-line reason when a call returns a non-OK status.  The serving calls, made
+several times a decode step on small inputs, are marshalled by the compiled
+``_binding`` module instead of through ctypes.  Every step of the
 computation runs in the library's CUDA kernels; there is no other path.  If
 the shared library has not been built, importing this package fails.
 """
@@ -166,6 +168,11 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _binding  # the serving calls' marshalling, built beside the library
+except ImportError as e:
+    raise ImportError(f"the binding module of {_HERE} is not built or was built for another torch ({e}); run "
+                      "__graft_entry__.build()") from e
 
 
 def _check(status: int) -> None:
@@ -548,52 +555,6 @@ def v4a_hca_attend_paged(q, ent_pool, ring, out, *, m: int, window: int, ctx_len
 # serving a batch: rotary positions, shared prefixes, eviction
 # ----------------------------------------------------------------------
 
-def _same_device(**tensors) -> torch.device:
-    """The one CUDA device of these tensors (None: an argument that was left out)."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libv4a takes CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return dev
-
-
-def _typed(t, name: str, dtype, shape) -> None:
-    """A contiguous tensor of this dtype and shape (None passes)."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    _contig(t, name)
-
-
-def _status_word(t) -> None:
-    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
-        raise ValueError("dev_status must be int32 with one element")
-
-
-def _float_dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
-
-
-def _enqueue(device, stream, call) -> None:
-    """Run call(stream pointer) with `device` current: by default on its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
-        return
-    with torch.cuda.device(device):
-        _check(call(_stream(stream)))
-
-
 def v4a_rope(pairs, *, rope_dims: int, positions=None, pos0: int = 0, pos_step: int = 1, rope_offset=None,
              rope_base: float = 10000.0, half: bool = False, inverse: bool = False, factor: float = 1.0,
              orig_ctx: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, out_scale: float = 1.0,
@@ -604,54 +565,8 @@ def v4a_rope(pairs, *, rope_dims: int, positions=None, pos0: int = 0, pos_step: 
     [batch][n_tok], or None for pos0 + i * pos_step.  half: pairs (k, k + R/2) instead of (2k, 2k + 1).
     inverse: by minus the angle, which is also the gradient of the forward call.  factor (and orig_ctx: YaRN)
     scale the frequencies for long contexts, out_scale multiplies the rotated dims."""
-    if not pairs:
-        return
-    ios = (RopeIO * len(pairs))()
-    named = {"positions": positions}
-    B = T = None
-    for i, (x, out) in enumerate(pairs):
-        if x.dim() not in (3, 4) or x.shape != out.shape or x.dtype != out.dtype:
-            raise ValueError("x and out must be [batch][n_tok][heads][d] or [batch][n_tok][d], of one shape and dtype")
-        if B is None:
-            B, T = int(x.shape[0]), int(x.shape[1])
-        elif (B, T) != (x.shape[0], x.shape[1]):
-            raise ValueError("the streams of a call have the same batch and tokens")
-        d = int(x.shape[-1])
-        if d > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1):
-            raise ValueError("x and out must have dense rows")
-        four = x.dim() == 4
-        named[f"x[{i}]"], named[f"out[{i}]"] = x, out
-        off = d - int(rope_dims) if rope_offset is None else int(rope_offset)
-        ios[i] = RopeIO(_ptr(x), _ptr(out), int(x.shape[2]) if four else 1, d, off, _float_dtype(x), x.stride(0),
-                        x.stride(1), x.stride(2) if four else 0, out.stride(0), out.stride(1),
-                        out.stride(2) if four else 0)
-    device = _same_device(**named)
-    if positions is not None:
-        if positions.dtype != torch.int64 or tuple(positions.shape) != (B, T):
-            raise ValueError("positions must be int64 [batch][n_tok]")
-        if T > 1 and positions.stride(1) != 1:
-            raise ValueError("positions must have dense rows")
-    par = RopeParams(int(rope_dims), int(bool(half)), int(bool(inverse)), float(rope_base), float(factor),
-                     int(orig_ctx), float(beta_fast), float(beta_slow), float(out_scale))
-    _enqueue(device, stream, lambda st: lib.v4a_rope(
-        ios, len(pairs), B, T, _ptr(positions), positions.stride(0) if positions is not None else 0, int(pos0),
-        int(pos_step), ctypes.byref(par), st))
-
-
-def _shared_cache(q, prefix, own, ring, n_prefix, own_count, own_entry, ctx_lens) -> SharedCache:
-    B, T, H, d = q.shape
-    if own is not None:
-        _typed(own, "own", q.dtype, (B, own.shape[1], d))
-    rows = int(own.shape[1]) if own is not None else 0
-    _typed(own_count, "own_count", torch.int32, (B,))
-    _typed(own_entry, "own_entry", torch.int32, (B, rows))
-    _typed(ctx_lens, "ctx_lens", torch.int64, (B,))
-    if prefix is not None:
-        _typed(prefix, "prefix", q.dtype, (prefix.shape[0], d))
-    if ring is not None:
-        _typed(ring, "ring", q.dtype, (B, ring.shape[1], d))
-    return SharedCache(_ptr(prefix), n_prefix, _ptr(own), rows, _ptr(own_count), _ptr(own_entry), _ptr(ring),
-                       int(ring.shape[1]) if ring is not None else 0, _ptr(ctx_lens))
+    _check(_binding.rope(pairs, rope_dims, positions, pos0, pos_step, rope_offset, rope_base, half, inverse, factor,
+                         orig_ctx, beta_fast, beta_slow, out_scale, stream))
 
 
 def v4a_shared_workspace_size(*, batch: int, n_q: int = 1, heads: int, d: int, n_prefix: int, own_rows: int,
@@ -670,29 +585,8 @@ def v4a_hca_attend_shared(q, prefix, own, ring, out, *, m: int, window: int, ctx
     [batch][ring_rows][d]; sequences are ctx_lens[b] tokens long (int64; None: ctx_len).  prefix, own and ring
     may be None.  out: float32, or bfloat16 with bfloat16 inputs; lse (float32 [batch][n_q][heads], optional)
     receives the log of the softmax denominator."""
-    _contig(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [batch][n_q][heads][d]")
-    B, T, H, d = q.shape
-    device = _same_device(q=q, prefix=prefix, own=own, ring=ring, out=out, ctx_lens=ctx_lens, own_count=own_count,
-                          own_entry=own_entry, lse=lse, workspace=workspace, dev_status=dev_status, sink=sink)
-    n_prefix = int(prefix.shape[0]) if prefix is not None else 0
-    cache = _shared_cache(q, prefix, own, ring, n_prefix, own_count, own_entry, ctx_lens)
-    _typed(out, "out", out.dtype, q.shape)
-    _typed(lse, "lse", torch.float32, (B, T, H))
-    _typed(sink, "sink", torch.float32, (H,))
-    _status_word(dev_status)
-    s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, window=window, ctx_len=ctx_len)
-    if workspace is None:
-        workspace = _workspace(lib.v4a_shared_workspace_size(ctypes.byref(s), n_prefix, cache.own_rows,
-                                                             _float_dtype(q)), device)
-    else:
-        _contig(workspace, "workspace")
-    ext = _ext(sink, rope_dims, rope_base)
-    _enqueue(device, stream, lambda st: lib.v4a_hca_attend_shared(
-        _ptr(q), ctypes.byref(cache), _ptr(out), _float_dtype(out), _ptr(lse), _float_dtype(q), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(dev_status), ctypes.byref(ext) if ext is not None else None,
-        ctypes.byref(s), st))
+    _check(_binding.hca_attend_shared(q, prefix, own, ring, out, m, window, ctx_len, ctx_lens, own_count, own_entry,
+                                      lse, workspace, dev_status, sink, rope_dims, rope_base, stream))
 
 
 def v4a_attend_weights(q, own, lse, weights, out, *, m: int, ctx_len: int, n_prefix: int = 0, ctx_lens=None,
@@ -700,21 +594,8 @@ def v4a_attend_weights(q, own, lse, weights, out, *, m: int, ctx_len: int, n_pre
     """out[b][i] = decay * weights[b][i] + what own slot i received of the attention of q, whose softmax
     denominators are exp(lse) (v4a_hca_attend_shared's lse).  weights and out: float32 [batch][own_rows], may be
     the same tensor; weights may be None with decay = 0.  Slots beyond own_count are left as they were."""
-    _contig(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [batch][n_q][heads][d]")
-    B, T, H, d = q.shape
-    device = _same_device(q=q, own=own, lse=lse, weights=weights, out=out, ctx_lens=ctx_lens, own_count=own_count,
-                          own_entry=own_entry, dev_status=dev_status)
-    cache = _shared_cache(q, None, own, None, int(n_prefix), own_count, own_entry, ctx_lens)
-    _typed(lse, "lse", torch.float32, (B, T, H))
-    _typed(weights, "weights", torch.float32, (B, cache.own_rows))
-    _typed(out, "out", torch.float32, (B, cache.own_rows))
-    _status_word(dev_status)
-    s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, ctx_len=ctx_len)
-    _enqueue(device, stream, lambda st: lib.v4a_attend_weights(
-        _ptr(q), ctypes.byref(cache), _ptr(lse), _ptr(weights), _ptr(out), float(decay), _float_dtype(q),
-        _ptr(dev_status), ctypes.byref(s), st))
+    _check(_binding.attend_weights(q, own, lse, weights, out, m, ctx_len, n_prefix, ctx_lens, own_count, own_entry,
+                                   decay, dev_status, stream))
 
 
 def v4a_evict(own, weights, own_out, weights_out, kept, count_out, *, budget: int, keep_first: int = 0,
@@ -724,24 +605,5 @@ def v4a_evict(own, weights, own_out, weights_out, kept, count_out, *, budget: in
     weights -- and move rows, weights and entry numbers, in order, to the front of own_out [batch][out_rows][d],
     weights_out and entry_out [batch][out_rows].  kept: int32 [batch][budget], the slots kept, -1 behind them;
     count_out: int32 [batch].  Output rows behind the kept ones are left as they were."""
-    if own.dim() != 3 or own_out.dim() != 3:
-        raise ValueError("own and own_out must be [batch][rows][d]")
-    device = _same_device(own=own, weights=weights, own_out=own_out, weights_out=weights_out, kept=kept,
-                          count_out=count_out, own_count=own_count, own_entry=own_entry, entry_out=entry_out,
-                          dev_status=dev_status)
-    B, rows, d = own.shape
-    out_rows = int(own_out.shape[1])
-    _contig(own, "own")
-    _typed(weights, "weights", torch.float32, (B, rows))
-    _typed(own_count, "own_count", torch.int32, (B,))
-    _typed(own_entry, "own_entry", torch.int32, (B, rows))
-    _typed(own_out, "own_out", own.dtype, (B, out_rows, d))
-    _typed(weights_out, "weights_out", torch.float32, (B, out_rows))
-    _typed(entry_out, "entry_out", torch.int32, (B, out_rows))
-    _typed(kept, "kept", torch.int32, (B, budget))
-    _typed(count_out, "count_out", torch.int32, (B,))
-    _status_word(dev_status)
-    io = EvictIO(_ptr(own), _ptr(weights), _ptr(own_count), _ptr(own_entry), rows, d, _float_dtype(own), _ptr(own_out),
-                 _ptr(weights_out), _ptr(entry_out), _ptr(kept), _ptr(count_out), out_rows, int(first_entry))
-    _enqueue(device, stream, lambda st: lib.v4a_evict(ctypes.byref(io), B, int(budget), int(keep_first),
-                                                      int(keep_recent), _ptr(dev_status), st))
+    _check(_binding.evict(own, weights, own_out, weights_out, kept, count_out, budget, keep_first, keep_recent,
+                          own_count, own_entry, entry_out, first_entry, dev_status, stream))

@@ -1,5 +1,7 @@
 """Build libv4a.so in-tree from csrc/*.cu for sm_100a (nvcc, one object per
-source compiled in parallel, then one shared-library link)."""
+source compiled in parallel, then one shared-library link), and _binding.so
+from csrc/binding.cpp (the CPython module that marshals the serving calls'
+tensors into it)."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -13,6 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libv4a.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -52,7 +55,33 @@ def build(verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
+    build_binding()
     return LIB
+
+
+def build_binding() -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(ROOT, "include", "v4a.h"), os.path.abspath(__file__)]
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(d) for d in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    includes = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for i in includes for x in ("-isystem" if i != includes[0] else "-I", i)], src, "-o", BINDING,
+           f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           f"-L{HERE}", "-l:libv4a.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
+    return BINDING
 
 
 if __name__ == "__main__":
