@@ -2,10 +2,11 @@
 //
 // Pair k of a row at position p turns by the angle p f_k, f_k = base^(-2k/R) (scaled for long contexts
 // on the host).  What is read and written once bounds it: 2 d elements per row (2 R in place), against
-// 3 flops per rotated element.  The angles are per token, not per row, so a block takes one token (or
-// a part of its rows), works out the token's R/2 (cos, sin) once into shared memory, and streams rows:
-// one thread per 8 elements (16 bytes of bf16), four in flight.  A decode step has few tokens; their
-// rows are then cut over several blocks, each with its own copy of the 32 angles.
+// 3 flops per rotated element.  An item is 8 elements of a row (16 bytes of bf16).  A thread keeps one
+// column of items and runs down the heads of its token, so the column's angles stay in registers, the
+// copied columns pass through as they are, and no index is worked out per item.  A block takes one
+// token, or several where their rows are few; its (cos, sin) are made once in shared memory while
+// the first rows are on their way.  With few tokens (a decode step) a token's heads are cut over blocks.
 #include <math.h>
 
 #include "common.cuh"
@@ -17,13 +18,17 @@ namespace {
 constexpr int kMaxStreams = 8;
 constexpr int kMaxPairs = 256;
 constexpr int kThreads = 256;
+constexpr int kTable = 8 * kThreads;  // angles of a block's tokens at most
 
 struct RopeStream {
     const void* x;
     void* out;
-    int heads, d, off;
-    int rot, row_items;  // items of a row: rotated ones first, then the copied chunks
-    int parts;           // blocks per token
+    int heads, off;
+    int rot, row_items;  // items of a row: rotated ones first, then the copied ones
+    // vectors: tokens per block (1 unless a token's rows fill less than half of it), heads side by side in it, and the
+    // blocks that a token's heads and columns are cut over; any alignment: blocks per token (h_parts)
+    int tokens, h_par, h_parts, c_parts;
+    unsigned block0;     // its first block
     long long xb, xt, xh, ob, ot, oh;
 };
 
@@ -32,6 +37,7 @@ struct RopeArgs {
     double f_hi[kMaxPairs];  // turns (not radians) per position, as a sum of two
     float f_lo[kMaxPairs];
     int n, n_tok, pairs, half, inverse;
+    unsigned all_tok;        // batch * n_tok
     float scale;
     const int64_t* positions;
     long long pos_stride, pos0, pos_step;
@@ -48,93 +54,139 @@ __device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
     return make_float2(c, s);
 }
 
-__device__ __forceinline__ void block_table(const RopeArgs& a, int b, int t, float2* cs) {
-    const int k = threadIdx.x;
-    if (k < a.pairs) {
+// (cos, sin) of n tokens from `tok` on: cs[i * pairs + k]
+__device__ __forceinline__ void make_table(const RopeArgs& a, unsigned tok, int n, float2* cs) {
+    for (int i = threadIdx.x; i < n * a.pairs; i += kThreads) {
+        const int k = i % a.pairs;
+        const unsigned at = tok + i / a.pairs, b = at / (unsigned)a.n_tok, t = at % (unsigned)a.n_tok;
         const long long p = a.positions ? a.positions[b * a.pos_stride + t] : a.pos0 + t * a.pos_step;
-        float2 v = turn((double)p, a.f_hi[k], a.f_lo[k]);
-        cs[k] = make_float2(v.x * a.scale, (a.inverse ? -v.y : v.y) * a.scale);
+        const float2 v = turn((double)p, a.f_hi[k], a.f_lo[k]);
+        cs[i] = make_float2(v.x * a.scale, (a.inverse ? -v.y : v.y) * a.scale);
     }
     __syncthreads();
 }
 
-// the stream and the part of it that this block takes
-__device__ __forceinline__ int which_stream(const RopeArgs& a, int& part) {
-    part = blockIdx.y;
+__device__ __forceinline__ const RopeStream& which_stream(const RopeArgs& a) {
     int k = 0;
-    while (part >= a.s[k].parts) part -= a.s[k++].parts;
-    return k;
+    while (k + 1 < a.n && blockIdx.x >= a.s[k + 1].block0) ++k;
+    return a.s[k];
 }
+
+// 8 elements as they lie in memory
+template <typename T>
+struct Item {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const { Vec8<T>::load(reinterpret_cast<const T*>(w), f); }
+    __device__ __forceinline__ void set(const float (&f)[8]) { Vec8<T>::store(reinterpret_cast<T*>(w), f); }
+};
 
 // Rows, offsets and strides in multiples of 8 elements: an item is one 8-element chunk, or, in the half
 // layout, the two chunks that a rotated item pairs up.
-template <typename T>
+template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float2 cs[kMaxPairs];
+    __shared__ __align__(16) float2 cs[kTable];
     griddep_wait();  // everything before this kernel on the stream has finished
-    int part;
-    const RopeStream& s = a.s[which_stream(a, part)];
-    const int b = blockIdx.x / a.n_tok, t = blockIdx.x % a.n_tok;
-    const T* xt = static_cast<const T*>(s.x) + b * s.xb + t * s.xt;
-    T* ot = static_cast<T*>(s.out) + b * s.ob + t * s.ot;
-    const int R = 2 * a.pairs;
-    const unsigned items = (unsigned)s.heads * s.row_items;
-    const unsigned per = (items + s.parts - 1) / s.parts;
-    const unsigned i0 = part * per, i1 = min(items, i0 + per);
-    constexpr int kU = 4;
-    bool table = false;
-    for (unsigned base = i0; base < i1 || !table; base += kU * kThreads) {
-        float u[kU][8], v[kU][8];
-        long long at[kU];
-        int pair[kU];  // first pair of a rotated item, -1 for a copied chunk, -2 for none
+    const RopeStream& s = which_stream(a);
+    const int parts = s.h_parts * s.c_parts;
+    const unsigned local = blockIdx.x - s.block0, group = local / (unsigned)parts;
+    const int part = (int)(local % (unsigned)parts), c_part = part % s.c_parts;
+    const unsigned tok0 = group * (unsigned)s.tokens;
+    const int n_tok = (int)min((unsigned)s.tokens, a.all_tok - tok0);
+    // this thread's column c, token and first head
+    int c, h, i_tok = 0;
+    bool on;
+    if (s.c_parts > 1) {
+        c = c_part * kThreads + threadIdx.x;
+        h = part / s.c_parts;
+        on = c < s.row_items;
+    } else {
+        const int r = (int)threadIdx.x / s.row_items;
+        c = (int)threadIdx.x - r * s.row_items;
+        if (s.tokens > 1) {
+            i_tok = r / s.heads;
+            h = r - i_tok * s.heads;
+            on = i_tok < n_tok;
+        } else {
+            h = part * s.h_par + r;
+            on = r < s.h_par;
+        }
+    }
+    const int step = s.h_par * s.h_parts;  // tokens > 1: all heads at once
+    const unsigned tok = tok0 + i_tok, b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
+    const bool rotated = c < s.rot;
+    int e = 8 * (rotated ? c : c - s.rot);
+    if (rotated) e += s.off;
+    else if (e >= s.off) e += 2 * a.pairs;
+    const T* xp = static_cast<const T*>(s.x) + b * s.xb + t * s.xt + e;
+    T* op = static_cast<T*>(s.out) + b * s.ob + t * s.ot + e;
+    constexpr int kU = sizeof(T) == 2 ? 4 : 2;  // rows in flight
+    constexpr int kA = HALF ? 8 : 4;            // pairs of an item
+    if (!on) h = s.heads;
+    Item<T> u[kU], v[kU];
+    auto load = [&]() {
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
-            const unsigned i = base + j * kThreads + threadIdx.x;
-            pair[j] = -2;
-            if (i >= i1) continue;
-            const unsigned h = i / (unsigned)s.row_items, c = i % (unsigned)s.row_items;
-            int e;
-            if ((int)c < s.rot) {
-                e = s.off + 8 * c;
-                pair[j] = a.half ? 8 * c : 4 * c;
-            } else {
-                e = 8 * (c - s.rot);
-                if (e >= s.off) e += R;
-                pair[j] = -1;
-            }
-            const T* xp = xt + h * s.xh + e;
-            Vec8<T>::load(xp, u[j]);
-            if (a.half && pair[j] >= 0) Vec8<T>::load(xp + a.pairs, v[j]);
-            at[j] = h * s.oh + e;
+            const int hj = h + j * step;
+            if (hj >= s.heads) continue;
+            u[j].load(xp + hj * s.xh);
+            if (HALF && rotated) v[j].load(xp + hj * s.xh + a.pairs);
         }
-        if (!table) {  // the first loads are in flight while the angles are worked out
-            block_table(a, b, t, cs);
-            table = true;
+    };
+    load();  // on its way while the angles are worked out
+    make_table(a, tok0, n_tok, cs);
+    float2 w[kA];
+    if (on && rotated) {
+#pragma unroll
+        for (int k = 0; k < kA; k += 2) {
+            const float4 x = *reinterpret_cast<const float4*>(&cs[i_tok * a.pairs + kA * c + k]);
+            w[k] = make_float2(x.x, x.y);
+            w[k + 1] = make_float2(x.z, x.w);
+        }
+    }
+    while (h < s.heads) {
+        if (rotated) {
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                if (h + j * step >= s.heads) continue;
+                float x[8], y[8];
+                u[j].get(x);
+                if (HALF) {
+                    v[j].get(y);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float p = x[k], q = y[k];
+                        x[k] = p * w[k % kA].x - q * w[k % kA].y;
+                        y[k] = q * w[k % kA].x + p * w[k % kA].y;
+                    }
+                    v[j].set(y);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float p = x[2 * k], q = x[2 * k + 1];
+                        x[2 * k] = p * w[k].x - q * w[k].y;
+                        x[2 * k + 1] = q * w[k].x + p * w[k].y;
+                    }
+                }
+                u[j].set(x);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
-            if (pair[j] == -2) continue;
-            T* op = ot + at[j];
-            if (pair[j] >= 0 && a.half) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 w = cs[pair[j] + e];
-                    const float x = u[j][e], y = v[j][e];
-                    u[j][e] = x * w.x - y * w.y;
-                    v[j][e] = y * w.x + x * w.y;
-                }
-                Vec8<T>::store(op + a.pairs, v[j]);
-            } else if (pair[j] >= 0) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 w = cs[pair[j] + e];
-                    const float x = u[j][2 * e], y = u[j][2 * e + 1];
-                    u[j][2 * e] = x * w.x - y * w.y;
-                    u[j][2 * e + 1] = y * w.x + x * w.y;
-                }
-            }
-            Vec8<T>::store(op, u[j]);
+            const int hj = h + j * step;
+            if (hj >= s.heads) continue;
+            u[j].store(op + hj * s.oh);
+            if (HALF && rotated) v[j].store(op + hj * s.oh + a.pairs);
         }
+        h += kU * step;
+        load();
     }
     // The attention kernels read their first query before they wait for this grid (they may, once all its
     // blocks have ended): the rows have reached L2 by then.  For the same reason there is no early
@@ -147,14 +199,15 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 cs[kMaxPairs];
     griddep_wait();
-    int part;
-    const RopeStream& s = a.s[which_stream(a, part)];
-    const int b = blockIdx.x / a.n_tok, t = blockIdx.x % a.n_tok;
+    const RopeStream& s = which_stream(a);
+    const unsigned local = blockIdx.x - s.block0, tok = local / (unsigned)s.h_parts;
+    const int part = (int)(local % (unsigned)s.h_parts);
+    const unsigned b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
     const T* xt = static_cast<const T*>(s.x) + b * s.xb + t * s.xt;
     T* ot = static_cast<T*>(s.out) + b * s.ob + t * s.ot;
-    block_table(a, b, t, cs);
+    make_table(a, tok, 1, cs);
     const unsigned items = (unsigned)s.heads * s.row_items;
-    const unsigned per = (items + s.parts - 1) / s.parts;
+    const unsigned per = (items + s.h_parts - 1) / s.h_parts;
     const unsigned i0 = part * per, i1 = min(items, i0 + per);
     for (unsigned i = i0 + threadIdx.x; i < i1; i += kThreads) {
         const unsigned h = i / (unsigned)s.row_items, c = i % (unsigned)s.row_items;
@@ -268,7 +321,6 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         s.x = r.x;
         s.out = r.out;
         s.heads = r.heads;
-        s.d = r.d;
         s.off = r.rope_offset;
         s.xb = r.x_batch_stride;
         s.xt = r.x_tok_stride;
@@ -292,25 +344,43 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
     a.pos0 = pos0;
     a.pos_step = pos_step;
     frequencies(p, &a);
-    // Few tokens: cut each token's rows over enough blocks to fill the SMs (one pass of 256 threads x 4 items is
-    // the least worth a block); many tokens: a block per token and stream.
     const long long tokens = (long long)batch * n_tok;
-    long long want = (8LL * kNumSMs + tokens - 1) / tokens;
-    int blocks_y = 0;
+    a.all_tok = (unsigned)tokens;
+    const long long want = (8LL * kNumSMs + tokens - 1) / tokens;  // blocks per token that fill the SMs
+    long long blocks = 0;
     for (int i = 0; i < n_streams; ++i) {
         RopeStream& s = a.s[i];
         s.rot = vec ? p.rope_dims / (p.half ? 16 : 8) : a.pairs;
         s.row_items = s.rot + (vec ? s.row_items / 8 : s.row_items);
-        const long long items = (long long)s.heads * s.row_items;
-        const long long most = (items + kThreads - 1) / kThreads;
-        s.parts = (int)(want < most ? want : most);
-        if (s.parts > 65535 / kMaxStreams) s.parts = 65535 / kMaxStreams;
-        blocks_y += s.parts;
+        s.tokens = s.h_par = s.c_parts = 1;
+        long long most;  // blocks that a token's heads can be cut over
+        if (!vec) {
+            most = ((long long)s.heads * s.row_items + kThreads - 1) / kThreads;
+        } else if (s.row_items > kThreads) {
+            s.c_parts = (s.row_items + kThreads - 1) / kThreads;
+            most = s.heads;
+        } else if ((long long)s.heads * s.row_items <= kThreads / 2) {
+            s.h_par = s.heads;
+            s.tokens = kThreads / (s.heads * s.row_items);
+            if (s.tokens > kTable / a.pairs) s.tokens = kTable / a.pairs;
+            if (s.tokens > tokens) s.tokens = (int)tokens;
+            most = 1;
+        } else {
+            s.h_par = kThreads / s.row_items;
+            if (s.h_par > s.heads) s.h_par = s.heads;
+            most = (s.heads + s.h_par - 1) / s.h_par;
+        }
+        s.h_parts = (int)(want < most ? want : most);
+        if (s.h_parts > 65535) s.h_parts = 65535;
+        s.block0 = (unsigned)blocks;
+        blocks += (tokens + s.tokens - 1) / s.tokens * s.h_parts * s.c_parts;
     }
-    const dim3 grid((unsigned)tokens, (unsigned)blocks_y);
+    if (blocks > 0x7fffffffLL) return report(V4A_ERR_UNSUPPORTED, "v4a_rope: too many rows for one call");
+    const dim3 grid((unsigned)blocks);
     const bool f32 = io[0].dtype == V4A_F32;
-    auto* kernel = vec ? (f32 ? rope_vec_kernel<float> : rope_vec_kernel<__nv_bfloat16>)
-                       : (f32 ? rope_any_kernel<float> : rope_any_kernel<__nv_bfloat16>);
+    auto* kernel = !vec     ? (f32 ? rope_any_kernel<float> : rope_any_kernel<__nv_bfloat16>)
+                   : p.half ? (f32 ? rope_vec_kernel<float, true> : rope_vec_kernel<__nv_bfloat16, true>)
+                            : (f32 ? rope_vec_kernel<float, false> : rope_vec_kernel<__nv_bfloat16, false>);
     cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? V4A_OK : report(V4A_ERR_CUDA, "v4a_rope: %s", cudaGetErrorString(e));
