@@ -2,11 +2,12 @@
 //
 // Of a sequence's n slots the `budget` heaviest stay (the first and last ones always), moved to the front
 // in order.  The rows that stay are read and written once: that copy bounds the call.  Choosing them is
-// a radix select over order-preserving 32-bit keys of the weights, by a cluster of blocks per sequence
-// (8 for long caches, so that one SM need not read all weights): three histogram passes of 11, 11 and 10
-// bits, summed over the cluster through distributed shared memory, then one ordered pass in which a
-// thread counts and places the slots of its own contiguous run.  evict_rows_kernel then moves the rows,
-// a warp per row, four rows in flight.
+// a radix select over order-preserving 32-bit keys of the weights, by a block per sequence, or a cluster
+// of up to 8 where a block's threads would have more than 8 keys each (what a cluster adds is a barrier and reads of
+// the other blocks' counts per pass).  The keys are loaded once and stay in registers: three histogram passes of 11, 11 and
+// 10 bits, the counts of a cluster's blocks added up through distributed shared memory, then one ordered
+// pass that places the slots by ballots.  evict_rows_kernel then moves the rows, a warp per row, four rows
+// in flight.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -33,10 +34,10 @@ struct EvictArgs {
 };
 
 struct EvictSmem {
-    uint32_t hist[kBins];   // this block's counts
+    uint32_t hist[3][kBins];  // this block's counts, by pass
     uint32_t warp[32];
-    uint32_t pick[4];       // chosen digit, how many of it are still wanted
-    uint32_t total[2];      // this block's slots above the threshold, and at it
+    uint32_t pick[2];         // chosen digit, how many of it are still wanted
+    uint32_t total[2];        // this block's slots above the threshold, and at it
 };
 
 // exclusive prefix sum over the block's threads; *sum: the block's total
@@ -66,12 +67,21 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_s, uin
     return before + x - v;
 }
 
+// V: keys per thread, in registers; 0: any number of them (n / (blocks * threads), rounded up), read again in every pass.
+// Slots ascend over blocks, then warps, then a warp's rounds, then lanes.
+template <int V>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     __shared__ EvictSmem sm;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
     griddep_wait();  // everything before this kernel on the stream has finished
     griddep_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto sync_all = [&] {
+        if (csize > 1) cluster.sync();
+        else __syncthreads();
+    };
     const int b = blockIdx.x / csize;
     int n = a.own_rows;
     if (a.own_count) {
@@ -80,39 +90,55 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         if (c != n && a.dev_status && threadIdx.x == 0 && crank == 0) atomicExch(a.dev_status, (int)V4A_ERR_DEVICE_FAULT);
     }
     const int want = n < a.budget ? n : a.budget;
+    const bool all = want == n;
     const float* w = a.weights + (long long)b * a.own_rows;
-    // this thread's run of slots; runs ascend over threads, then blocks
-    const int run = (int)(((long long)n + (long long)csize * kThreads - 1) / ((long long)csize * kThreads));
-    const long long r0 = ((long long)crank * kThreads + threadIdx.x) * run;
-    const int s0 = (int)(r0 < n ? r0 : n), s1 = (int)(r0 + run < n ? r0 + run : n);
-    auto key_of = [&](int i) -> uint32_t {
+    const int rounds = V ? V : (int)(((long long)n + (long long)csize * kThreads - 1) / ((long long)csize * kThreads));
+    const long long base = ((long long)crank * kThreads + warp * 32) * rounds + lane;
+    auto make_key = [&](long long i) -> uint32_t {
         if (i < a.first || i >= n - a.recent) return 0xffffffffu;  // always kept
         const float x = w[i];
-        if (isnan(x)) return 0u;
-        const uint32_t k = float_to_ordered(x);  // -inf: 0x007fffff, +inf: 0xff800000
-        return k;
+        return isnan(x) ? 0u : float_to_ordered(x);  // -inf: 0x007fffff, +inf: 0xff800000
     };
+    uint32_t keys[V ? V : 1];
+    if (V && !all) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) keys[j] = base + 32 * j < n ? make_key(base + 32 * j) : 0u;
+    }
+    auto key = [&](int j) -> uint32_t { return V ? keys[V ? j : 0] : make_key(base + 32LL * j); };
     // radix select of the want-th largest key; digits of 11, 11 and 10 bits
     uint32_t prefix = 0, need = (uint32_t)want;
-    if (want > 0 && want < n) {
+    if (!all) {
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t digits = pass == 2 ? 1024u : 2048u;
             const uint32_t above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
-            for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
-            __syncthreads();
-            for (int i = s0; i < s1; ++i) {
-                const uint32_t k = key_of(i);
-                if (((k ^ prefix) & above) == 0) atomicAdd(&sm.hist[(k >> shift) & (digits - 1)], 1u);
+            uint32_t* hist = sm.hist[pass];
+            if (pass == 0) __syncthreads();  // the counts are zero
+#pragma unroll
+            for (int j = 0; j < (V ? V : rounds); ++j) {
+                const bool in = base + 32LL * j < n;
+                const uint32_t k = in ? key(j) : 0u, d = (k >> shift) & (digits - 1);
+                const bool mine = in && ((k ^ prefix) & above) == 0;
+                const uint32_t m = __ballot_sync(0xffffffffu, mine);
+                if (m == 0) continue;
+                // equal weights are common, and 32 additions to one counter slow
+                const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
+                if (__all_sync(0xffffffffu, !mine || d == d0)) {
+                    if (lane == 0) atomicAdd(&hist[d0], (uint32_t)__popc(m));
+                } else if (mine) {
+                    atomicAdd(&hist[d], 1u);
+                }
             }
-            cluster.sync();
+            sync_all();
             // this thread's two bins, the highest digits first
             uint32_t c[2] = {0, 0};
             const uint32_t d0 = digits - 1 - 2 * threadIdx.x;
             if (2 * threadIdx.x < digits) {
-                for (int r = 0; r < csize; ++r) {
-                    const uint32_t* h = cluster.map_shared_rank(sm.hist, r);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (r >= csize) continue;
+                    const uint32_t* h = csize > 1 ? cluster.map_shared_rank(hist, r) : hist;
                     c[0] += h[d0];
                     c[1] += h[d0 - 1];
                 }
@@ -124,59 +150,61 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
                 sm.pick[0] = second ? d0 - 1 : d0;
                 sm.pick[1] = need - before - (second ? c[0] : 0u);
             }
-            cluster.sync();  // pick is written, and no block still reads this pass's counts
+            __syncthreads();
             prefix |= sm.pick[0] << shift;
             need = sm.pick[1];
-            __syncthreads();
         }
     }
-    // slots above the threshold stay, and the first `need` of those at it
-    const bool all = want == n;
-    uint32_t gt = 0, eq = 0;
-    for (int i = s0; i < s1; ++i) {
-        if (all) {
-            ++gt;
-        } else if (want > 0) {
-            const uint32_t k = key_of(i);
-            gt += k > prefix;
-            eq += k == prefix;
-        }
+    // Slots above the threshold stay, and the first `need` of those at it; with all of them, every slot counts as above.
+    auto above = [&](int j) { return base + 32LL * j < n && (all || key(j) > prefix); };
+    auto equal = [&](int j) { return base + 32LL * j < n && !all && key(j) == prefix; };
+    uint32_t gt = 0, eq = 0;  // of this warp
+#pragma unroll
+    for (int j = 0; j < (V ? V : rounds); ++j) {
+        gt += __popc(__ballot_sync(0xffffffffu, above(j)));
+        eq += __popc(__ballot_sync(0xffffffffu, equal(j)));
     }
     uint32_t sum_gt, sum_eq;
-    uint32_t at_gt = block_scan(gt, sm.warp, &sum_gt), at_eq = block_scan(eq, sm.warp, &sum_eq);
-    if (threadIdx.x == 0) {
-        sm.total[0] = sum_gt;
-        sm.total[1] = sum_eq;
-    }
-    cluster.sync();
-    for (int r = 0; r < crank; ++r) {
-        const uint32_t* t = cluster.map_shared_rank(sm.total, r);
-        at_gt += t[0];
-        at_eq += t[1];
+    uint32_t at_gt = block_scan(lane == 0 ? gt : 0u, sm.warp, &sum_gt), at_eq = block_scan(lane == 0 ? eq : 0u, sm.warp, &sum_eq);
+    at_gt = __shfl_sync(0xffffffffu, at_gt, 0);
+    at_eq = __shfl_sync(0xffffffffu, at_eq, 0);
+    if (csize > 1) {
+        if (threadIdx.x == 0) {
+            sm.total[0] = sum_gt;
+            sm.total[1] = sum_eq;
+        }
+        cluster.sync();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r >= crank) continue;
+            const uint32_t* t = cluster.map_shared_rank(sm.total, r);
+            at_gt += t[0];
+            at_eq += t[1];
+        }
     }
     int32_t* kept = a.kept + (long long)b * a.budget;
     const long long orow = (long long)b * a.out_rows;
-    for (int i = s0; i < s1; ++i) {
-        uint32_t pos;  // the slots kept before this one
-        const uint32_t k = all ? 1u : want > 0 ? key_of(i) : 0u;
-        if (all || (want > 0 && k > prefix)) {
-            pos = at_gt++ + (at_eq < need ? at_eq : need);
-        } else if (want > 0 && k == prefix) {
-            const uint32_t r = at_eq++;
-            if (r >= need) continue;
-            pos = at_gt + r;
-        } else {
-            continue;
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int j = 0; j < (V ? V : rounds); ++j) {
+        const bool is_gt = above(j), is_eq = equal(j);
+        const uint32_t m_gt = __ballot_sync(0xffffffffu, is_gt), m_eq = __ballot_sync(0xffffffffu, is_eq);
+        const uint32_t g = at_gt + __popc(m_gt & below), r = at_eq + __popc(m_eq & below);
+        at_gt += __popc(m_gt);
+        at_eq += __popc(m_eq);
+        if (is_gt || (is_eq && r < need)) {
+            const uint32_t pos = g + (r < need ? r : need);  // the slots kept before this one
+            const int i = (int)(base + 32LL * j);
+            kept[pos] = i;
+            a.weights_out[orow + pos] = w[i];
+            if (a.entry_out)
+                a.entry_out[orow + pos] = a.own_entry ? a.own_entry[(long long)b * a.own_rows + i] : a.first_entry + i;
         }
-        kept[pos] = i;
-        a.weights_out[orow + pos] = w[i];
-        if (a.entry_out)
-            a.entry_out[orow + pos] = a.own_entry ? a.own_entry[(long long)b * a.own_rows + i] : a.first_entry + i;
     }
     // pad the list
     for (long long i = (long long)want + crank * kThreads + threadIdx.x; i < a.budget; i += (long long)csize * kThreads) kept[i] = -1;
     if (crank == 0 && threadIdx.x == 0) a.count_out[b] = want;
-    cluster.sync();  // no block leaves while another may read its shared memory
+    if (csize > 1) cluster.sync();  // no block leaves while another may read its shared memory
 }
 
 // One warp per four output rows of a sequence: 16-byte chunks, up to two per lane and row in flight.
@@ -266,22 +294,12 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     a.first = keep_first;
     a.recent = keep_recent;
     a.first_entry = io->first_entry;
-    // a cluster of up to 8 blocks (the portable size) per sequence: as many as leave each thread a slot
+    // a cluster of up to 8 blocks (the portable size) per sequence: as many as leave each thread at most 8 keys
     int cs = 1;
-    while (cs < 8 && (long long)cs * kThreads < io->own_rows) cs *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(batch * cs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cs;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    while (cs < 8 && (long long)cs * kThreads * 8 < io->own_rows) cs *= 2;
+    const long long per = ((long long)io->own_rows + cs * kThreads - 1) / (cs * kThreads);
+    auto* kernel = per <= 1 ? evict_select_kernel<1> : per <= 8 ? evict_select_kernel<8> : per <= 32 ? evict_select_kernel<32> : evict_select_kernel<0>;
+    cudaError_t e = launch_pdl_cluster(kernel, dim3((unsigned)(batch * cs)), dim3(kThreads), 0, st, cs, a);
     if (e == cudaSuccess && io->own_rows > 0)
         e = launch_pdl(evict_rows_kernel, dim3((unsigned)((budget + 31) / 32), (unsigned)batch), dim3(256), 0, st,
                        static_cast<const uint4*>(io->own), static_cast<uint4*>(io->own_out), (const int32_t*)io->kept,
