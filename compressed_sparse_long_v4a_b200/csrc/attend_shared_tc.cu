@@ -10,7 +10,7 @@
 //
 // A range goes to a CTA pair (two SMs, cta_group::2), each CTA holding 64 of the 128 rows.  Per tile
 //     S  = Q K^T   M = 128 rows x N = 64 keys x K = 512    (each CTA brings 32 of the keys)
-//     P  = softmax(S), two threads per row, lazily rescaled maximum
+//     P  = softmax(S), four threads per row, lazily rescaled maximum
 //     O += P V     M = 128 x N = 2 x 256 dims x K = 64 keys (each CTA brings half of the dims)
 // With 64 rows of 512 dims a CTA's O is half of tensor memory, and 64 rows at the full rate of the tensor
 // cores need the pair: alone a CTA runs M = 64 at half rate.  Since S wants all dims of half of the keys and
@@ -27,7 +27,8 @@
 // key; such a tile's V is scrubbed of non-finite values before the product (0 x NaN would spoil the rows of
 // other sequences).  Rows that do see the key have a NaN in P, or weight 0 for a logit of -inf.
 //
-// Warps: 0 loads Q and X, 6 loads Z, 1 (of CTA 0) issues the MMAs, 2-5 run the softmax and write pieces.
+// Warps: 0 loads Q and X, 10 loads Z, 1 and 11 of CTA 0 issue the MMAs, 1 of CTA 1 reports that Z is there, 2-9 run the
+// softmax and write pieces.
 // Every wait is bounded; on a time-out both CTAs record a device fault, their pieces become NaN and they
 // wind down.  Pieces (m, l, O) are merged by shared_tc_join_kernel: out = sum_i e^{m_i - m} o_i / l.
 #include <cudaTypedefs.h>
@@ -45,11 +46,11 @@ constexpr int kRows = 128;          // rows of a group
 constexpr int kHalf = 64;           // ... of one CTA
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kStages = 4;
-constexpr int kSBufs = 3;
+constexpr int kSBufs = 4;
 constexpr int kPairs = kNumSMs / 2;
 constexpr uint32_t kXBytes = 32 * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
 constexpr uint32_t kColS = 256, kColsS = 32, kTmemCols = 512;  // O: columns 0-255
-constexpr int kThreads = 7 * 32;
+constexpr int kThreads = 12 * 32;
 constexpr long long kStall = 1LL << 31;  // cycles without progress after which the MMA warp gives up
 constexpr float kSlack = 8.0f;           // keep a stale running max until the true one exceeds it by 2^8
 constexpr uint32_t kIdescQK = tc::idesc_f16(128, kKeys, 0, 0), kIdescPV = tc::idesc_f16(128, 256, 0, 1);
@@ -58,14 +59,17 @@ struct __align__(1024) Smem {
     uint8_t q[kQBytes];
     uint8_t kv[kStages][kXBytes];
     uint8_t p[2][kHalf * 128];
-    float mx[2][4][32];  // row maxima of a tile's halves, by tile parity
-    float ls[4][32];
+    float mx[2][4][kHalf];  // row maxima of a tile's quarters, by tile parity
+    float ls[4][kHalf];
     // x_full, z_ready, p_full and q_full count in CTA 0 only
     uint64_t x_full[kStages], z_full[kStages], z_ready[kStages], kv_empty[kStages], s_full[kSBufs], p_full[2], p_free[2];
     uint64_t q_full, q_empty, drain;
+    uint32_t flags[kStages];  // of the tile in a stage, for the MMA warp
     int abort_flag;
     uint32_t tmem_base;
 };
+
+enum : uint32_t { kFirst = 1, kLast = 2, kEnd = 4, kNone = 8 };  // of its piece; last of the range; no tile in it at all
 
 struct PairArgs {
     SharedArgs a;
@@ -74,6 +78,7 @@ struct PairArgs {
     long long total;       // tiles of all groups
     unsigned rows, per_seq, lcm;  // batch * n_q * heads; n_q * heads; least common multiple of that and 128
     int groups, pairs;
+    int pre_tail;          // keys of the prefix's last tile
     int pre, own, win;     // tiles: prefix; own and window of a sequence (win: one more than the window fills, for a
                            // ring that wraps inside it)
     float scale_log2;
@@ -140,7 +145,22 @@ struct Walk {
             enter_sequence(c);
         }
     }
-    __device__ bool next(const PairArgs& c, Tile& t) {
+    __device__ __forceinline__ bool next(const PairArgs& c, Tile& t) {
+        if (!fresh && i < c.pre && left > 0) {  // the common step: from one prefix tile to the next
+            t.kind = kPrefix;
+            t.group = g;
+            t.first = false;
+            t.b = 0;
+            t.y = i * kKeys;
+            t.p0 = t.y;
+            t.n = ++i == c.pre ? c.pre_tail : kKeys;
+            --left;
+            if (i == c.pre && i < per) enter_sequence(c);
+            return true;
+        }
+        return next_any(c, t);
+    }
+    __device__ bool next_any(const PairArgs& c, Tile& t) {
         while (left > 0) {
             if (i == per) {
                 ++g;
@@ -153,8 +173,7 @@ struct Walk {
             if (i < c.pre) {
                 t.kind = kPrefix;
                 t.y = i * kKeys;
-                const long long n = c.a.n_prefix - t.y;
-                t.n = n < kKeys ? (int)n : kKeys;
+                t.n = i + 1 == c.pre ? c.pre_tail : kKeys;
                 t.b = 0;
                 t.p0 = t.y;
                 if (++i == c.pre && i < per) enter_sequence(c);
@@ -217,10 +236,14 @@ struct Maps {
 __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal(), once = tc::l2_stream_policy((int)((c.per_seq + kRows - 1) / kRows));
     Walk walk(c, pair);
-    Tile t;
+    Tile t, nxt;
     int j = 0, piece = 0;
-    bool ok = true;
-    while (walk.next(c, t)) {
+    bool ok = true, more = walk.next(c, t);
+    if (!more && rank == 0) {
+        sm.flags[0] = kNone;
+        tc::mbar_arrive(&sm.x_full[0]);
+    }
+    for (; more; t = nxt) {
         if (aborted(sm)) { ok = false; break; }
         if (t.first) {
             if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1)) { ok = false; break; }
@@ -230,7 +253,11 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
         }
         const int st = j % kStages;
         if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st], (j / kStages - 1) & 1)) { ok = false; break; }
-        if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
+        more = walk.next(c, nxt);
+        if (rank == 0) {
+            sm.flags[st] = (t.first ? kFirst : 0u) | (!more || nxt.first ? kLast : 0u) | (more ? 0u : kEnd);
+            tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
+        }
         tc::tma_load_4d_pair(sm.kv[st], &maps.x[t.kind], 0, t.y + (int)rank * 32, 0, t.b, tc::peer_addr(&sm.x_full[st], 0),
                              t.kind == kPrefix ? again : once);
         ++j;
@@ -241,105 +268,115 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
     }
 }
 
-// warp 6, one lane: the other CTA's 32 keys of this CTA's slabs, once S has been computed
+// warp 10, one lane: the other CTA's 32 keys of this CTA's slabs, once S has been computed
 __device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal();
+    const uint32_t other = rank ^ 1;
     Walk walk(c, pair);
     Tile t;
-    int j = 0;
-    bool ok = true, more = true;
-    for (;; ++j) {
-        more = ok && !aborted(sm) && walk.next(c, t);
-        if (more && !tc::mbar_wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) ok = more = false;
-        if (more) {
-            const int st = j % kStages;
-            const uint32_t other = rank ^ 1;
-            tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
+    for (int j = 0; walk.next(c, t); ++j) {
+        const int st = j % kStages;
+        if (aborted(sm) || !tc::mbar_wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) {
+            fault(sm, c, rank);
+            break;
+        }
+        tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
 #pragma unroll 1
-            for (int u = 0; u < 4; ++u)
-                tc::tma_load_4d(sm.kv[st] + 8192 * u + 4096 * other, &maps.z[t.kind], 0, t.y + (int)other * 32, 2 * u + (int)rank,
-                                t.b, &sm.z_full[st], again);
-        }
-        if (j > 0) {  // the tile before has landed meanwhile
-            const int st = (j - 1) % kStages;
-            if (!tc::mbar_wait(&sm.z_full[st], ((j - 1) / kStages) & 1)) ok = false;
-            else {
-                tc::fence_proxy_async();
-                tc::peer_arrive(tc::peer_addr(&sm.z_ready[st], 0));
-            }
-        }
-        if (!more) break;
+        for (int u = 0; u < 4; ++u)
+            tc::tma_load_4d(sm.kv[st] + 8192 * u + 4096 * other, &maps.z[t.kind], 0, t.y + (int)other * 32, 2 * u + (int)rank, t.b,
+                            &sm.z_full[st], again);
     }
-    if (!ok) fault(sm, c, rank);
+}
+
+// warp 1 of CTA 1, one lane: tells CTA 0 that Z has landed here
+__device__ void pass_on_z(Smem& sm, const PairArgs& c, int pair) {
+    const uint32_t ready = tc::peer_addr(&sm.z_ready[0], 0);
+    Walk walk(c, pair);
+    Tile t;
+    for (int j = 0; walk.next(c, t); ++j) {
+        const int st = j % kStages;
+        if (aborted(sm) || !tc::mbar_wait(&sm.z_full[st], (j / kStages) & 1)) {
+            fault(sm, c, 1);
+            break;
+        }
+        tc::fence_proxy_async();
+        tc::peer_arrive(ready + 8 * st);
+    }
 }
 
 // ---------------------------------------------------------------------
-// warp 1 of CTA 0: every MMA of the pair, in whatever order its inputs become ready
+// CTA 0, warps 1 and 11: every MMA of the pair, S and O by a warp each, so that the waits of one are filled by the
+// other's products.  The code is kept small: these loops run between those of the softmax, and a line of
+// instructions fetched again costs more than an MMA (all 40 of a tile unrolled, a copy per stage, took 75 cycles
+// each to issue, rolled 44; the smaller ones execute in 26).
 // ---------------------------------------------------------------------
 __device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+    bool ok = false;
+    for (uint32_t i = 0; i < tc::kWaitPolls && !ok; ++i) ok = tc::mbar_try_cluster(bar, parity);
+    return __all_sync(0xffffffffu, ok);
+}
 
-__device__ void issue(Smem& sm, const PairArgs& c, uint32_t tmem, int pair) {
+// S = Q K^T: A = Q (64 rows per CTA), B = 32 keys per CTA
+__device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
+    static_assert(kStages == kSBufs, "one S buffer per stage: a stage that is free again means that its S was read");
+    const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024), b0 = tc::sw128_desc(tc::smem_u32(sm.kv), 16, 1024);
+    int pieces = 0;
+    bool ok = true;
+    for (int j = 0;; ++j) {
+        const int st = j % kStages;
+        ok = wait_cluster(&sm.x_full[st], (uint32_t)(j / kStages) & 1);
+        if (!ok) break;
+        const uint32_t flags = __shfl_sync(0xffffffffu, sm.flags[st], 0);
+        if (flags & kNone) break;
+        if (flags & kFirst) ok = wait_cluster(&sm.q_full, pieces++ & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint64_t a = a0, b = dadd(b0, st * kXBytes);
+        const uint32_t d = tmem + kColS + kColsS * st;
+#pragma unroll 1
+        for (int s = 0; s < 8; ++s) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc::mma_f16_pair(d, dadd(a, kk * 32), dadd(b, kk * 32), kIdescQK, (uint32_t)(s | kk));
+            a = dadd(a, 8192);
+            b = dadd(b, 4096);
+        }
+        tc::mma_commit_pair(&sm.s_full[st]);
+        if (flags & kLast) tc::mma_commit_pair(&sm.q_empty);
+        if (flags & kEnd) break;
+    }
+    if (!ok) fault(sm, c, 0);
+    tc::mma_commit_pair(&sm.drain);
+}
+// O += P V: A = P (64 rows of 128 bytes per CTA), B = 16 keys x 128 dims (2 slabs, 8 KB apart) per CTA
+__device__ void issue_o(Smem& sm, const PairArgs& c, uint32_t tmem, int pair) {
+    const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.p), 16, 1024), b0 = tc::sw128_desc(tc::smem_u32(sm.kv), 8192, 1024);
     Walk walk(c, pair);
-    Tile t, nxt;
-    bool more = walk.next(c, t), ok = true;
-    int jq = 0, jp = 0, pieces = 0;
-    uint32_t firsts = 0;  // by tile modulo 32: first of its piece
-    const uint64_t q0 = tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024);
-    long long t_last = clock64();
-    while (more || jp < jq) {
-        if (__shfl_sync(0xffffffffu, (int)aborted(sm), 0)) { ok = false; break; }
-        bool progressed = false;
-        if (jp < jq && tc::mbar_test_warp_cluster(&sm.p_full[jp & 1], (uint32_t)(jp >> 1) & 1) &&
-            tc::mbar_test_warp_cluster(&sm.z_ready[jp % kStages], (uint32_t)(jp / kStages) & 1)) {
-            tc::tc_fence_after();
-            const int st = jp % kStages;
-            // A = P (64 rows of 128 bytes per CTA); B = V, 16 keys x 128 dims (2 slabs, 8 KB apart) per CTA
-            const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.p[jp & 1]), 16, 1024);
-            const uint64_t b0 = tc::sw128_desc(tc::smem_u32(sm.kv[st]), 8192, 1024);
-            const bool first = (firsts >> (jp & 31)) & 1;
+    Tile t;
+    bool ok = true;
+    for (int j = 0; __any_sync(0xffffffffu, walk.next(c, t)); ++j) {
+        const int st = j % kStages;
+        const uint32_t phase = (uint32_t)(j / kStages) & 1, fresh = __any_sync(0xffffffffu, t.first);
+        ok = wait_cluster(&sm.z_full[st], phase) && wait_cluster(&sm.z_ready[st], phase) && wait_cluster(&sm.p_full[j & 1], (uint32_t)(j >> 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint64_t a = dadd(a0, (j & 1) * (kHalf * 128)), b = dadd(b0, st * kXBytes);
+#pragma unroll 1
+        for (int kk = 0; kk < kKeys / 16; ++kk) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    tc::mma_f16_pair(tmem + 128 * h, dadd(a0, kk * 32), dadd(b0, 16384 * h + kk * 2048), kIdescPV,
-                                     (!first || kk > 0) ? 1u : 0u);
-            tc::mma_commit_pair(&sm.kv_empty[st]);
-            tc::mma_commit_pair(&sm.p_free[jp & 1]);
-            ++jp;
-            progressed = true;
-        } else if (more && jq - jp < kSBufs && tc::mbar_test_warp_cluster(&sm.x_full[jq % kStages], (uint32_t)(jq / kStages) & 1) &&
-                   (!t.first || tc::mbar_test_warp_cluster(&sm.q_full, pieces & 1))) {
-            tc::tc_fence_after();
-            const uint64_t k0 = tc::sw128_desc(tc::smem_u32(sm.kv[jq % kStages]), 16, 1024);
-            const uint32_t d_s = tmem + kColS + kColsS * (jq % kSBufs);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_f16_pair(d_s, dadd(q0, s * 8192 + kk * 32), dadd(k0, s * 4096 + kk * 32), kIdescQK,
-                                     (s | kk) ? 1u : 0u);
-            tc::mma_commit_pair(&sm.s_full[jq % kSBufs]);
-            firsts = (firsts & ~(1u << (jq & 31))) | ((uint32_t)t.first << (jq & 31));
-            pieces += t.first;
-            more = walk.next(c, nxt);
-            if (!more || nxt.first) tc::mma_commit_pair(&sm.q_empty);  // the last S of this piece
-            t = nxt;
-            ++jq;
-            progressed = true;
+            for (int h = 0; h < 2; ++h) tc::mma_f16_pair(tmem + 128 * h, a, dadd(b, 16384 * h), kIdescPV, (uint32_t)kk | (fresh ^ 1));
+            a = dadd(a, 32);
+            b = dadd(b, 2048);
         }
-        if (progressed) {
-            t_last = clock64();
-        } else if (__shfl_sync(0xffffffffu, (int)(clock64() - t_last > kStall), 0)) {
-            ok = false;
-            break;
-        }
+        tc::mma_commit_pair(&sm.kv_empty[st]);
+        tc::mma_commit_pair(&sm.p_free[j & 1]);
     }
     if (!ok) fault(sm, c, 0);
     tc::mma_commit_pair(&sm.drain);
 }
 
 // ---------------------------------------------------------------------
-// warps 2-5: softmax, rescaling, pieces
+// warps 2-9: softmax, rescaling, pieces
 // ---------------------------------------------------------------------
 __device__ __forceinline__ uint32_t low_bits(long long n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
@@ -350,13 +387,24 @@ __device__ __forceinline__ uint32_t scrub(uint32_t x) {
     return x;
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results below the normal range become 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, uint32_t rank) {
     const SharedArgs& a = c.a;
-    const int sub = (threadIdx.x >> 5) & 3;  // TMEM lanes 32 sub ..: rows 32 (sub & 1) .., keys or dims of half sub >> 1
-    const int lane = threadIdx.x & 31, half = sub >> 1, r = 32 * (sub & 1) + lane;
-    const int bar = 1 + (sub & 1);  // the two warps that share rows
+    // TMEM lanes 32 sub ..: rows 32 (sub & 1) .., of a tile's keys (and of O's slabs) half sub >> 1; the second
+    // four warps take the second 16 of those keys.  So four threads share a row, each a quarter of the keys.
+    const int sub = (threadIdx.x >> 5) & 3, wg = (threadIdx.x - 64) >> 7;
+    const int lane = threadIdx.x & 31, half = sub >> 1, r = 32 * (sub & 1) + lane, quarter = 2 * half + wg;
+    const int key0 = 16 * quarter;
+    const int bar = 1 + (sub & 1);  // the four warps that share rows
     const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
-    const uint32_t p_full[2] = {tc::peer_addr(&sm.p_full[0], 0), tc::peer_addr(&sm.p_full[1], 0)};
+    const uint32_t p_full0 = tc::peer_addr(&sm.p_full[0], 0);
+    uint8_t* const prow = sm.p[0] + (r >> 3) * 1024 + (r & 7) * 128;
+    const uint32_t chunk0 = ((2 * quarter) ^ (r & 7)) << 4, chunk1 = ((2 * quarter + 1) ^ (r & 7)) << 4;
     Walk walk(c, pair);
     Tile t, nxt;
     bool more = walk.next(c, t), ok = true;
@@ -367,7 +415,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
     long long pos = 0, seen = 0;
     bool alive = false;
     auto wait = [&](uint64_t* bar_, uint32_t parity) {
-        if (ok && (aborted(sm) || !tc::mbar_wait(bar_, parity))) ok = false;
+        if (ok) ok = tc::mbar_wait(bar_, parity);
         ok = __all_sync(0xffffffffu, ok);
         return ok;
     };
@@ -386,65 +434,64 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 seen = seen_entries(a, pos);
             }
         }
-        // this thread's 32 keys
-        uint32_t mask = 0;
-        const int n = t.n - 32 * half;
-        if (t.kind == kPrefix) {
-            mask = alive ? low_bits(n) : 0u;
-        } else if (t.kind == kOwn) {
-            const bool mine = alive && b == t.b;
-            if (a.own_entry) {
-                int e = -1;
-                if (lane < n) e = a.own_entry[(long long)t.b * a.own_rows + t.p0 + 32 * half + lane];
+        // this thread's 16 keys
+        uint32_t mask = alive ? 0xffffu : 0u;
+        if (t.kind != kPrefix || t.n < kKeys) {
+            const int n = t.n - key0;
+            if (t.kind == kPrefix) {
+                mask &= low_bits(n);
+            } else if (t.kind == kOwn) {
+                const bool mine = alive && b == t.b;
+                if (a.own_entry) {
+                    int e = -1;
+                    if (lane < 16 && lane < n) e = a.own_entry[(long long)t.b * a.own_rows + t.p0 + key0 + lane];
+                    mask = 0;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int ek = __shfl_sync(0xffffffffu, e, k);
-                    mask |= (uint32_t)(ek >= 0 && ek < seen) << k;
+                    for (int k = 0; k < 16; ++k) {
+                        const int ek = __shfl_sync(0xffffffffu, e, k);
+                        mask |= (uint32_t)(ek >= 0 && ek < seen) << k;
+                    }
+                    if (!mine) mask = 0;
+                } else {
+                    const long long lim = seen - a.n_prefix - t.p0 - key0;
+                    mask = mine ? mask & low_bits(lim < n ? lim : n) : 0u;
                 }
-                if (!mine) mask = 0;
-            } else if (mine) {
-                const long long lim = seen - a.n_prefix - t.p0 - 32 * half;
-                mask = low_bits(lim < n ? lim : n);
+            } else {
+                const long long from = pos - a.window + 1 - t.p0 - key0, to = pos + 1 - t.p0 - key0;
+                mask = alive && b == t.b ? mask & low_bits(to < n ? to : n) & ~low_bits(from) : 0u;
             }
-        } else if (alive && b == t.b) {
-            const long long from = pos - a.window + 1 - t.p0 - 32 * half, to = pos + 1 - t.p0 - 32 * half;
-            mask = low_bits(to < n ? to : n) & ~low_bits(from);
         }
-        float x[32];
+        float x[16];
         if (wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) {
             tc::tc_fence_after();
-            uint32_t u[32];
-            tc::tmem_ld_x32(lanes + kColS + kColsS * (j % kSBufs), u);
+            uint32_t u[16];
+            tc::tmem_ld_x16(lanes + kColS + kColsS * (j % kSBufs) + 16 * wg, u);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(u[k]);
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(u[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = 0.f;
+            for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
         bool odd = false;  // a key of this tile is not finite
         if (t.kind != kPrefix) {
             float d = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) d = fmaf(x[k], 0.f, d);
+            for (int k = 0; k < 16; ++k) d = fmaf(x[k], 0.f, d);
             odd = !(d == 0.f);
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (mask == ~0u) {
+        if (mask != 0xffffu) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                x[k] = (mask >> k) & 1 ? x[k] : -INFINITY;
-                mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
-            }
+            for (int k = 0; k < 16; ++k) x[k] = (mask >> k) & 1 ? x[k] : -INFINITY;
         }
-        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c.scale_log2;
-        sm.mx[j & 1][sub][lane] = mt;
-        if (t.kind == kPrefix) tc::named_barrier(bar, 64);
-        else odd = tc::named_barrier_or(3, 128, odd);
-        mt = fmaxf(mt, sm.mx[j & 1][sub ^ 2][lane]);
+        float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int k = 4; k < 16; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
+        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));  // of four NaN: NaN
+        sm.mx[j & 1][quarter][r] = mt;
+        if (t.kind == kPrefix) tc::named_barrier(bar, 128);
+        else odd = tc::named_barrier_or(3, 256, odd);
+        mt = fmaxf(fmaxf(sm.mx[j & 1][0][r], sm.mx[j & 1][1][r]), fmaxf(sm.mx[j & 1][2][r], sm.mx[j & 1][3][r])) * c.scale_log2;
         float alpha = 1.f;
         if (mt > m_run + kSlack) {
             if (m_run != -INFINITY) alpha = exp2f(m_run - mt);
@@ -452,42 +499,40 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         }
         l_run *= alpha;
         const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
-        uint32_t pk[16];
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[8];
+        float ls[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float p0 = exp2f(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2f(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
-            ls[k & 3] += p0 + p1;  // the sum is of the unrounded weights
+        for (int k = 0; k < 8; ++k) {
+            const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
+            ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
             const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
             pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
         }
-        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
-        if (rescale && wait(&sm.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {  // O is complete up to the tile before
+        l_run += ls[0] + ls[1];
+        if (__any_sync(0xffffffffu, alpha != 1.f) && wait(&sm.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+            // O, complete up to the tile before, follows the maximum: 128 columns of this warp's lanes
             tc::tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t o[64];
-                tc::tmem_ld_x64(lanes + 64 * q, o);
+            for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
+                uint32_t o[32];
+                tc::tmem_ld_x32(lanes + 32 * q, o);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tc::tmem_st_x64(lanes + 64 * q, o);
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tc::tmem_st_x32(lanes + 32 * q, o);
             }
             tc::tmem_st_wait();
         }
         // the P buffer of this parity is free once the product two tiles back is done
         if (j < 2 || wait(&sm.p_free[j & 1], ((j >> 1) - 1) & 1)) {
-            uint8_t* prow = sm.p[j & 1] + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(prow + (((4 * half + k) ^ (r & 7)) << 4)) =
-                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+            uint8_t* pr = prow + (j & 1) * (kHalf * 128);
+            *reinterpret_cast<uint4*>(pr + chunk0) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(pr + chunk1) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
         if (odd && wait(&sm.z_full[j % kStages], (j / kStages) & 1)) {
-            // both halves of V are here: scrub it, a row of 128 bytes at a time
+            // both halves of V are here: scrub it
             uint4* v = reinterpret_cast<uint4*>(sm.kv[j % kStages]);
-            for (int k = threadIdx.x - 64; k < (int)(kXBytes / 16); k += 128) {
+            for (int k = threadIdx.x - 64; k < (int)(kXBytes / 16); k += 256) {
                 const uint4 w = v[k];
                 v[k] = make_uint4(scrub(w.x), scrub(w.y), scrub(w.z), scrub(w.w));
             }
@@ -495,32 +540,33 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         tc::fence_proxy_async();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) tc::peer_arrive(p_full[j & 1]);
+        if (lane == 0 && ok) tc::peer_arrive(p_full0 + 8 * (j & 1));
 
         more = walk.next(c, nxt);
         if (!more || nxt.first) {
             // write the piece
             const long long piece = pair + t.group;
             for (; next_group < t.group; ++next_group)  // groups of the range without a tile that holds anything
-                if (half == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
+                if (quarter == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
             next_group = t.group + 1;
-            sm.ls[sub][lane] = l_run;
-            tc::named_barrier(bar, 64);
-            if (half == 0) {
-                const float l = l_run + sm.ls[sub ^ 2][lane];
+            sm.ls[quarter][r] = l_run;
+            tc::named_barrier(bar, 128);
+            if (quarter == 0) {
+                const float l = (l_run + sm.ls[1][r]) + (sm.ls[2][r] + sm.ls[3][r]);
                 c.part_ml[piece * kRows + rank * kHalf + r] = make_float2(isnan(l) ? NAN : m_run, l);
             }
             if (wait(&sm.p_free[j & 1], (j >> 1) & 1)) {
                 tc::tc_fence_after();
                 float4* po = c.part_o + piece * (kRows * kD / 4) + rank * kHalf + r;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[64];
-                    tc::tmem_ld_x64(lanes + 64 * q, o);
+                for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
+                    uint32_t o[32];
+                    tc::tmem_ld_x32(lanes + 32 * q, o);
                     tc::tmem_ld_wait();
-                    float4* pq = po + (long long)(2 * q + half) * 16 * kRows;  // slab 2 q + half
+                    // columns 64 i .. of O are slab 2 i + half: 16 quads of dims
+                    float4* pq = po + (long long)((q & ~1) + half) * 16 * kRows + (q & 1) * 8 * kRows;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
+                    for (int k = 0; k < 8; ++k)
                         pq[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                 }
@@ -531,11 +577,11 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
     }
     const long long f1 = range_start(c, pair + 1);
     for (; next_group < c.groups && tiles_before(c, next_group) < f1; ++next_group)
-        if (half == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
+        if (quarter == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
     if (!ok || aborted(sm)) {
         fault(sm, c, rank);
         for (int g = c.g0[pair]; g < next_group; ++g)
-            if (half == 0) c.part_ml[(pair + (long long)g) * kRows + rank * kHalf + r] = make_float2(NAN, NAN);
+            if (quarter == 0) c.part_ml[(pair + (long long)g) * kRows + rank * kHalf + r] = make_float2(NAN, NAN);
     }
 }
 
@@ -549,17 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sm.x_full[i], 1);
             tc::mbar_init(&sm.z_full[i], 1);
-            tc::mbar_init(&sm.z_ready[i], 2);
+            tc::mbar_init(&sm.z_ready[i], 1);
             tc::mbar_init(&sm.kv_empty[i], 1);
         }
         for (int i = 0; i < kSBufs; ++i) tc::mbar_init(&sm.s_full[i], 1);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sm.p_full[i], 8);  // the softmax warps of both CTAs
+            tc::mbar_init(&sm.p_full[i], 16);  // the softmax warps of both CTAs
             tc::mbar_init(&sm.p_free[i], 1);
         }
         tc::mbar_init(&sm.q_full, 1);
         tc::mbar_init(&sm.q_empty, 1);
-        tc::mbar_init(&sm.drain, 1);
+        tc::mbar_init(&sm.drain, 2);  // both warps that issue
         sm.abort_flag = 0;
         tc::fence_barrier_init();
     }
@@ -572,10 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0) {
         if (lane == 0) load_x(sm, c, maps, pair, rank);
-    } else if (warp == 6) {
+    } else if (warp == 10) {
         if (lane == 0) load_z(sm, c, maps, pair, rank);
     } else if (warp == 1) {
-        if (rank == 0) issue(sm, c, tmem, pair);
+        if (rank == 0) issue_s(sm, c, tmem);
+        else if (lane == 0) pass_on_z(sm, c, pair);
+    } else if (warp == 11) {
+        if (rank == 0) issue_o(sm, c, tmem, pair);
     } else {
         softmax(sm, c, tmem, pair, rank);
     }
@@ -729,6 +778,7 @@ void plan(const SharedArgs& a, PairArgs* c) {
     c->lcm = lcm < 0xffffffffULL ? (unsigned)lcm : 0xffffffffu;  // beyond every row: divides to 0 either way
     c->groups = (int)((c->rows + kRows - 1) / kRows);
     c->pre = (int)((a.n_prefix + kKeys - 1) / kKeys);
+    c->pre_tail = (int)(a.n_prefix - (long long)(c->pre - 1) * kKeys);
     c->own = (a.own_rows + kKeys - 1) / kKeys;
     c->win = a.window > 0 ? (int)(((long long)a.window + a.n_q - 1 + kKeys - 1) / kKeys) + 1 : 0;
     c->total = tiles_before(*c, c->groups);

@@ -4,7 +4,7 @@
 // in order.  The rows that stay are read and written once: that copy bounds the call.  Choosing them is
 // a radix select over order-preserving 32-bit keys of the weights, by a block per sequence, or a cluster
 // of up to 8 where a block's threads would have more than 8 keys each (what a cluster adds is a barrier and reads of
-// the other blocks' counts per pass).  The keys are loaded once and stay in registers: three histogram passes of 11, 11 and
+// the other blocks' counts per pass).  The keys are loaded once and stay in shared memory: three histogram passes of 11, 11 and
 // 10 bits, the counts of a cluster's blocks added up through distributed shared memory, then one ordered
 // pass that places the slots by ballots.  evict_rows_kernel then moves the rows, a warp per row, four rows
 // in flight.
@@ -12,6 +12,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+
+#include <cstddef>
 
 namespace cg = cooperative_groups;
 
@@ -33,12 +35,14 @@ struct EvictArgs {
     int own_rows, out_rows, budget, first, recent, first_entry;
 };
 
-struct EvictSmem {
+struct __align__(16) EvictSmem {
     uint32_t hist[3][kBins];  // this block's counts, by pass
-    uint32_t warp[32];
-    uint32_t pick[2];         // chosen digit, how many of it are still wanted
     uint32_t total[2];        // this block's slots above the threshold, and at it
+    uint32_t pick[2];         // chosen digit, how many of it are still wanted
+    uint32_t warp[32];
 };
+
+static_assert(offsetof(EvictSmem, hist) % 8 == 0 && offsetof(EvictSmem, total) % 8 == 0, "read in pairs by other blocks");
 
 // exclusive prefix sum over the block's threads; *sum: the block's total
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_s, uint32_t* sum) {
@@ -67,12 +71,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_s, uin
     return before + x - v;
 }
 
-// V: keys per thread, in registers; 0: any number of them (n / (blocks * threads), rounded up), read again in every pass.
-// Slots ascend over blocks, then warps, then a warp's rounds, then lanes.
-template <int V>
+// STORED: the keys stay in (dynamic) shared memory, `rounds` per thread; else they are made again in every pass.
+// Slots ascend over blocks, then warps, then a warp's rounds, then lanes.  The loops are rolled: the code runs cold,
+// and fetching unrolled copies took most of the time (8 keys a thread in registers: 17 us instead of 7).
+template <bool STORED>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     __shared__ EvictSmem sm;
-    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+    extern __shared__ uint32_t stored[];
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
     griddep_wait();  // everything before this kernel on the stream has finished
     griddep_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
@@ -83,30 +89,32 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         else __syncthreads();
     };
     const int b = blockIdx.x / csize;
-    int n = a.own_rows;
+    unsigned n = (unsigned)a.own_rows;
     if (a.own_count) {
-        const int c = a.own_count[b];
-        n = c < 0 ? 0 : c > a.own_rows ? a.own_rows : c;
-        if (c != n && a.dev_status && threadIdx.x == 0 && crank == 0) atomicExch(a.dev_status, (int)V4A_ERR_DEVICE_FAULT);
+        const int c = a.own_count[b], in = c < 0 ? 0 : c > a.own_rows ? a.own_rows : c;
+        if (c != in && a.dev_status && threadIdx.x == 0 && crank == 0) atomicExch(a.dev_status, (int)V4A_ERR_DEVICE_FAULT);
+        n = (unsigned)in;
     }
-    const int want = n < a.budget ? n : a.budget;
+    const unsigned want = n < (unsigned)a.budget ? n : (unsigned)a.budget;
     const bool all = want == n;
     const float* w = a.weights + (long long)b * a.own_rows;
-    const int rounds = V ? V : (int)(((long long)n + (long long)csize * kThreads - 1) / ((long long)csize * kThreads));
-    const long long base = ((long long)crank * kThreads + warp * 32) * rounds + lane;
-    auto make_key = [&](long long i) -> uint32_t {
-        if (i < a.first || i >= n - a.recent) return 0xffffffffu;  // always kept
+    const unsigned width = (unsigned)csize * kThreads;
+    const int rounds = (int)((n + width - 1) / width);
+    const unsigned base = ((unsigned)crank * kThreads + warp * 32) * rounds + lane;
+    const unsigned first = (unsigned)a.first, free_slots = n > (unsigned)a.first + a.recent ? n - a.first - a.recent : 0;
+    auto make_key = [&](unsigned i) -> uint32_t {
+        if (i - first >= free_slots) return 0xffffffffu;  // always kept
         const float x = w[i];
         return isnan(x) ? 0u : float_to_ordered(x);  // -inf: 0x007fffff, +inf: 0xff800000
     };
-    uint32_t keys[V ? V : 1];
-    if (V && !all) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) keys[j] = base + 32 * j < n ? make_key(base + 32 * j) : 0u;
+    if (STORED && !all) {
+#pragma unroll 8
+        for (int j = 0; j < rounds; ++j)
+            if (base + 32 * j < n) stored[j * kThreads + threadIdx.x] = make_key(base + 32 * j);
     }
-    auto key = [&](int j) -> uint32_t { return V ? keys[V ? j : 0] : make_key(base + 32LL * j); };
+    auto key = [&](int j) -> uint32_t { return STORED ? stored[j * kThreads + threadIdx.x] : make_key(base + 32 * j); };
     // radix select of the want-th largest key; digits of 11, 11 and 10 bits
-    uint32_t prefix = 0, need = (uint32_t)want;
+    uint32_t prefix = 0, need = want;
     if (!all) {
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
@@ -115,15 +123,15 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             const uint32_t above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
             uint32_t* hist = sm.hist[pass];
             if (pass == 0) __syncthreads();  // the counts are zero
-#pragma unroll
-            for (int j = 0; j < (V ? V : rounds); ++j) {
-                const bool in = base + 32LL * j < n;
-                const uint32_t k = in ? key(j) : 0u, d = (k >> shift) & (digits - 1);
+#pragma unroll 1
+            for (int j = 0; j < rounds; ++j) {
+                const bool in = base + 32 * j < n;
+                const uint32_t k = in ? key(j) : 0u;
                 const bool mine = in && ((k ^ prefix) & above) == 0;
                 const uint32_t m = __ballot_sync(0xffffffffu, mine);
                 if (m == 0) continue;
                 // equal weights are common, and 32 additions to one counter slow
-                const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
+                const uint32_t d = (k >> shift) & (digits - 1), d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
                 if (__all_sync(0xffffffffu, !mine || d == d0)) {
                     if (lane == 0) atomicAdd(&hist[d0], (uint32_t)__popc(m));
                 } else if (mine) {
@@ -135,12 +143,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             uint32_t c[2] = {0, 0};
             const uint32_t d0 = digits - 1 - 2 * threadIdx.x;
             if (2 * threadIdx.x < digits) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    if (r >= csize) continue;
-                    const uint32_t* h = csize > 1 ? cluster.map_shared_rank(hist, r) : hist;
-                    c[0] += h[d0];
-                    c[1] += h[d0 - 1];
+                if (csize == 1) {
+                    c[0] = hist[d0];
+                    c[1] = hist[d0 - 1];
+                } else {
+#pragma unroll 4
+                    for (int r = 0; r < csize; ++r) {
+                        const uint2 h = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, r) + d0 - 1);
+                        c[0] += h.y;
+                        c[1] += h.x;
+                    }
                 }
             }
             uint32_t sum;
@@ -156,14 +168,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         }
     }
     // Slots above the threshold stay, and the first `need` of those at it; with all of them, every slot counts as above.
-    auto above = [&](int j) { return base + 32LL * j < n && (all || key(j) > prefix); };
-    auto equal = [&](int j) { return base + 32LL * j < n && !all && key(j) == prefix; };
-    uint32_t gt = 0, eq = 0;  // of this warp
-#pragma unroll
-    for (int j = 0; j < (V ? V : rounds); ++j) {
-        gt += __popc(__ballot_sync(0xffffffffu, above(j)));
-        eq += __popc(__ballot_sync(0xffffffffu, equal(j)));
+    uint32_t gt = 0, eq = 0;
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+        if (base + 32 * j >= n) continue;
+        const uint32_t k = all ? 0u : key(j);
+        gt += all || k > prefix;
+        eq += !all && k == prefix;
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);  // of this warp
+    eq = __reduce_add_sync(0xffffffffu, eq);
     uint32_t sum_gt, sum_eq;
     uint32_t at_gt = block_scan(lane == 0 ? gt : 0u, sm.warp, &sum_gt), at_eq = block_scan(lane == 0 ? eq : 0u, sm.warp, &sum_eq);
     at_gt = __shfl_sync(0xffffffffu, at_gt, 0);
@@ -174,36 +188,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             sm.total[1] = sum_eq;
         }
         cluster.sync();
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (r >= crank) continue;
-            const uint32_t* t = cluster.map_shared_rank(sm.total, r);
-            at_gt += t[0];
-            at_eq += t[1];
+        for (int r = 0; r < crank; ++r) {
+            const uint2 t = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sm.total, r));
+            at_gt += t.x;
+            at_eq += t.y;
         }
     }
     int32_t* kept = a.kept + (long long)b * a.budget;
     const long long orow = (long long)b * a.out_rows;
     const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-    for (int j = 0; j < (V ? V : rounds); ++j) {
-        const bool is_gt = above(j), is_eq = equal(j);
+#pragma unroll 2
+    for (int j = 0; j < rounds; ++j) {
+        const unsigned i = base + 32 * j;
+        const bool in = i < n;
+        const uint32_t k = in && !all ? key(j) : 0u;
+        const bool is_gt = in && (all || k > prefix), is_eq = in && !all && k == prefix;
         const uint32_t m_gt = __ballot_sync(0xffffffffu, is_gt), m_eq = __ballot_sync(0xffffffffu, is_eq);
         const uint32_t g = at_gt + __popc(m_gt & below), r = at_eq + __popc(m_eq & below);
         at_gt += __popc(m_gt);
         at_eq += __popc(m_eq);
         if (is_gt || (is_eq && r < need)) {
             const uint32_t pos = g + (r < need ? r : need);  // the slots kept before this one
-            const int i = (int)(base + 32LL * j);
-            kept[pos] = i;
+            kept[pos] = (int32_t)i;
             a.weights_out[orow + pos] = w[i];
             if (a.entry_out)
-                a.entry_out[orow + pos] = a.own_entry ? a.own_entry[(long long)b * a.own_rows + i] : a.first_entry + i;
+                a.entry_out[orow + pos] = a.own_entry ? a.own_entry[(long long)b * a.own_rows + i] : a.first_entry + (int)i;
         }
     }
     // pad the list
     for (long long i = (long long)want + crank * kThreads + threadIdx.x; i < a.budget; i += (long long)csize * kThreads) kept[i] = -1;
-    if (crank == 0 && threadIdx.x == 0) a.count_out[b] = want;
+    if (crank == 0 && threadIdx.x == 0) a.count_out[b] = (int32_t)want;
     if (csize > 1) cluster.sync();  // no block leaves while another may read its shared memory
 }
 
@@ -298,8 +312,11 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     int cs = 1;
     while (cs < 8 && (long long)cs * kThreads * 8 < io->own_rows) cs *= 2;
     const long long per = ((long long)io->own_rows + cs * kThreads - 1) / (cs * kThreads);
-    auto* kernel = per <= 1 ? evict_select_kernel<1> : per <= 8 ? evict_select_kernel<8> : per <= 32 ? evict_select_kernel<32> : evict_select_kernel<0>;
-    cudaError_t e = launch_pdl_cluster(kernel, dim3((unsigned)(batch * cs)), dim3(kThreads), 0, st, cs, a);
+    const bool keep = per <= 48;  // 4 KB each
+    auto* kernel = keep ? evict_select_kernel<true> : evict_select_kernel<false>;
+    const size_t smem = keep ? (size_t)per * kThreads * 4 : 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = launch_pdl_cluster(kernel, dim3((unsigned)(batch * cs)), dim3(kThreads), smem, st, cs, a);
     if (e == cudaSuccess && io->own_rows > 0)
         e = launch_pdl(evict_rows_kernel, dim3((unsigned)((budget + 31) / 32), (unsigned)batch), dim3(256), 0, st,
                        static_cast<const uint4*>(io->own), static_cast<uint4*>(io->own_out), (const int32_t*)io->kept,

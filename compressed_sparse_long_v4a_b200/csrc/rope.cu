@@ -18,7 +18,7 @@ namespace {
 constexpr int kMaxStreams = 8;
 constexpr int kMaxPairs = 256;
 constexpr int kThreads = 256;
-constexpr int kTable = 8 * kThreads;  // angles of a block's tokens at most
+constexpr int kTable = kThreads;  // angles of a block's tokens at most: one per thread
 
 struct RopeStream {
     const void* x;
@@ -54,13 +54,21 @@ __device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
     return make_float2(c, s);
 }
 
-// (cos, sin) of n tokens from `tok` on: cs[i * pairs + k]
+// a parameter by its address: the lanes of a warp read neighbouring ones, which constant memory serialises
+template <typename X>
+__device__ __forceinline__ X by_address(const X* p) {
+    asm("" : "+l"(p));
+    return *p;
+}
+
+// (cos, sin) of n tokens from `tok` on: cs[i * pairs + k], one per thread
 __device__ __forceinline__ void make_table(const RopeArgs& a, unsigned tok, int n, float2* cs) {
-    for (int i = threadIdx.x; i < n * a.pairs; i += kThreads) {
+    const int i = threadIdx.x;
+    if (i < n * a.pairs) {
         const int k = i % a.pairs;
         const unsigned at = tok + i / a.pairs, b = at / (unsigned)a.n_tok, t = at % (unsigned)a.n_tok;
         const long long p = a.positions ? a.positions[b * a.pos_stride + t] : a.pos0 + t * a.pos_step;
-        const float2 v = turn((double)p, a.f_hi[k], a.f_lo[k]);
+        const float2 v = turn((double)p, by_address(&a.f_hi[k]), by_address(&a.f_lo[k]));
         cs[i] = make_float2(v.x * a.scale, (a.inverse ? -v.y : v.y) * a.scale);
     }
     __syncthreads();
@@ -91,7 +99,7 @@ struct Item {
 // Rows, offsets and strides in multiples of 8 elements: an item is one 8-element chunk, or, in the half
 // layout, the two chunks that a rotated item pairs up.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ __align__(16) float2 cs[kTable];
     griddep_wait();  // everything before this kernel on the stream has finished
     const RopeStream& s = which_stream(a);
