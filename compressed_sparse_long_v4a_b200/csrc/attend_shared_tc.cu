@@ -4,23 +4,25 @@
 //     out = sum_r p_r v_r,  p = softmax_r(q . v_r / sqrt(d)),  lse = log sum_r e^{q . v_r / sqrt(d)}
 //
 // Every query of the batch sees the whole prefix, so the rows (sequence, query, head) of all sequences are
-// one matrix, taken in groups of 128 that ignore where a sequence ends.  A group's keys are tiles of 64:
+// one matrix, taken in groups of 128 that ignore where a sequence ends.  A group's keys are tiles of 128:
 // the prefix, then the own slots and the window of each sequence that has rows in the group; rows of
 // other sequences are masked there.  The tiles of all groups form one flat sequence, cut into equal ranges.
 //
 // A range goes to a CTA pair (two SMs, cta_group::2), each CTA holding 64 of the 128 rows.  Per tile
-//     S  = Q K^T   M = 128 rows x N = 64 keys x K = 512    (each CTA brings 32 of the keys)
+//     S  = Q K^T   M = 128 rows x N = 128 keys x K = 512   (each CTA brings 64 of the keys)
 //     P  = softmax(S), four threads per row, lazily rescaled maximum
-//     O += P V     M = 128 x N = 2 x 256 dims x K = 64 keys (each CTA brings half of the dims)
+//     O += P V     M = 128 x N = 2 x 256 dims x K = 128 keys (each CTA brings half of the dims)
 // With 64 rows of 512 dims a CTA's O is half of tensor memory, and 64 rows at the full rate of the tensor
-// cores need the pair: alone a CTA runs M = 64 at half rate.  Since S wants all dims of half of the keys and
-// O half of the dims of all keys, a stage of 32 KB is used twice: it is loaded with this CTA's 32 keys
-// ("X"), and once S is done the slabs of dims that O does not need here make room for the other 32 keys
-// of those that it does ("Z").  So a tile costs 48 KB of loads per CTA and 32 KB of shared memory, and
-// four stages fit beside the 64 KB of queries.
+// cores need the pair (measured per MMA of K = 16: pair M = 128, N = 128: 32 cycles, N = 256: 66; one CTA, M = 64,
+// N = 64: 38, N = 128: 64).  Shared memory feeds both operands: with N = 64 it, not the tensor core, bounds S
+// (26 cycles instead of 16), hence tiles of 128 keys in two stages rather than 64 in four.
+// Since S wants all dims of half of the keys and O half of the dims of all keys, a stage of 64 KB is used
+// twice: it is loaded with this CTA's 64 keys ("X"), and once S is done the slabs of dims that O does not need
+// here make room for the other 64 keys of those that it does ("Z").  So a tile costs 96 KB of loads per CTA
+// and 64 KB of shared memory, and two stages fit beside the 64 KB of queries.
 //
-// Slabs are 64 dims (128 bytes) wide; slab s of the CTA's own keys lies at 4096 s.  CTA 0 has the even slabs
-// of O, CTA 1 the odd ones: block u (8192 u) becomes the 64 keys of slab 2 u + rank.
+// Slabs are 64 dims (128 bytes) wide; slab s of the CTA's own keys lies at 8192 s.  CTA 0 has the even slabs
+// of O, CTA 1 the odd ones: block u (16384 u) becomes the 128 keys of slab 2 u + rank.
 //
 // Masked places may hold anything.  A NaN or infinity in a row of K = V makes the raw S of every row of the
 // matrix non-finite at that key, so the softmax threads see it, also for rows that do not see the
@@ -44,36 +46,52 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRows = 128;          // rows of a group
 constexpr int kHalf = 64;           // ... of one CTA
-constexpr int kKeys = 64;           // keys of a tile
-constexpr int kStages = 4;
-constexpr int kSBufs = 4;
+constexpr int kKeys = 128;          // keys of a tile
+constexpr int kOwnKeys = 64;        // ... of which a CTA brings these for S
+constexpr int kStages = 2;          // and S buffers
 constexpr int kPairs = kNumSMs / 2;
-constexpr uint32_t kXBytes = 32 * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
-constexpr uint32_t kColS = 256, kColsS = 32, kTmemCols = 512;  // O: columns 0-255
+constexpr uint32_t kXBytes = kOwnKeys * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
+constexpr uint32_t kSlab = kOwnKeys * 128;  // 64 dims of a CTA's keys
+constexpr uint32_t kColS = 256, kColsS = 64, kTmemCols = 512;  // O: columns 0-255
 constexpr int kThreads = 12 * 32;
-constexpr long long kStall = 1LL << 31;  // cycles without progress after which the MMA warp gives up
 constexpr float kSlack = 8.0f;           // keep a stale running max until the true one exceeds it by 2^8
 constexpr uint32_t kIdescQK = tc::idesc_f16(128, kKeys, 0, 0), kIdescPV = tc::idesc_f16(128, 256, 0, 1);
+
+enum Kind { kPrefix, kOwn, kWindow };
+// first, last: of its piece; end: last of the range; none: the range holds nothing; same: a full tile of the
+// prefix behind another one
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kNone = 8, kSame = 16 };
+
+struct __align__(16) Tile {
+    int flags, kind;
+    int group, b;        // b: the sequence (own, window)
+    int y, n;            // first row of its 128 in prefix / own / ring, rows that count
+    long long p0;        // what row y holds: own slot, or position
+};
 
 struct __align__(1024) Smem {
     uint8_t q[kQBytes];
     uint8_t kv[kStages][kXBytes];
-    uint8_t p[2][kHalf * 128];
+    uint8_t p[2][kHalf * 128];  // by half of the keys
+    Tile tile[kStages];  // what each stage holds
     float mx[2][4][kHalf];  // row maxima of a tile's quarters, by tile parity
     float ls[4][kHalf];
     // x_full, z_ready, p_full and q_full count in CTA 0 only
-    uint64_t x_full[kStages], z_full[kStages], z_ready[kStages], kv_empty[kStages], s_full[kSBufs], p_full[2], p_free[2];
+    uint64_t told[kStages], x_full[kStages], z_full[kStages], z_ready[kStages], kv_empty[kStages], s_full[kStages];
+    uint64_t p_full, p_free;
     uint64_t q_full, q_empty, drain;
-    uint32_t flags[kStages];  // of the tile in a stage, for the MMA warp
     int abort_flag;
     uint32_t tmem_base;
 };
 
-enum : uint32_t { kFirst = 1, kLast = 2, kEnd = 4, kNone = 8 };  // of its piece; last of the range; no tile in it at all
+struct Range {
+    int g, i, n;   // a pair's first tile: its group and its place in it; how many tiles
+    int last;      // group of the last one
+};
 
 struct PairArgs {
     SharedArgs a;
-    float2* part_ml;       // [pieces][128] (m in base-2 logits, l)
+    float2* part_ml;       // [pieces][128] (m in base-2 logits, l); piece = pair + group
     float4* part_o;        // [pieces][128 quads of dims][128 rows]
     long long total;       // tiles of all groups
     unsigned rows, per_seq, lcm;  // batch * n_q * heads; n_q * heads; least common multiple of that and 128
@@ -82,45 +100,32 @@ struct PairArgs {
     int pre, own, win;     // tiles: prefix; own and window of a sequence (win: one more than the window fills, for a
                            // ring that wraps inside it)
     float scale_log2;
-    int g0[kPairs + 1];    // group of every pair's first tile
+    Range range[kPairs];
 };
 
-// tiles of the groups before g.  A group has `pre` tiles and own + win for every sequence with rows in it: one
+// Tiles of the groups before g (host).  A group has `pre` tiles and own + win for every sequence with rows in it: one
 // more than the sequences that begin inside it, behind its first row.
-__host__ __device__ inline long long tiles_before(const PairArgs& c, int g) {
+long long tiles_before(const PairArgs& c, int g) {
     if (g == 0) return 0;
     const unsigned long long e = (unsigned long long)g * kRows;
     const unsigned last = (unsigned)(e < c.rows ? e : c.rows) - 1;
     const long long seqs = g + (long long)(last / c.per_seq) - (long long)(last / c.lcm);
     return (long long)g * c.pre + seqs * (c.own + c.win);
 }
-__device__ __forceinline__ long long range_start(const PairArgs& c, int pair) { return (long long)pair * c.total / c.pairs; }
 
-enum Kind { kPrefix, kOwn, kWindow };
-
-struct Tile {
-    int group, kind, b;  // b: the sequence (own, window)
-    int y, n;            // first row of its 64 in prefix / own / ring, rows that count
-    long long p0;        // what row y holds: own slot, or position
-    bool first;          // first tile of its piece
-};
-
-// walks the tiles of a range that hold anything, the same in every role
+// walks the tiles of a range that hold anything
 struct Walk {
-    long long left;
-    int g, i, per, seq0, seqs;  // group, tile in it, its tiles, its sequences
+    int left, g, i, per;        // tiles to go; group, tile in it, its tiles
     int s, w;                   // sequence and its tile
-    bool fresh;
+    bool fresh;                 // no tile of this group yet
     int count, row0, n_a, n_w;  // own slots; window: ring row of position lo, positions before the ring's end, all
     long long lo;
 
     __device__ void enter_group(const PairArgs& c) {
         const unsigned r0 = (unsigned)g * kRows, r1 = min(r0 + kRows, c.rows) - 1;
-        seq0 = (int)(r0 / c.per_seq);
-        seqs = (int)(r1 / c.per_seq) - seq0 + 1;
-        per = c.pre + seqs * (c.own + c.win);
+        s = (int)(r0 / c.per_seq);
+        per = c.pre + ((int)(r1 / c.per_seq) - s + 1) * (c.own + c.win);
         fresh = true;
-        s = seq0;
         w = 0;
     }
     __device__ void enter_sequence(const PairArgs& c) {
@@ -133,34 +138,19 @@ struct Walk {
         n_a = n_w < c.a.ring_rows - row0 ? n_w : c.a.ring_rows - row0;
     }
     __device__ Walk(const PairArgs& c, int pair) {
-        const long long f0 = range_start(c, pair);
-        left = range_start(c, pair + 1) - f0;
-        g = c.g0[pair];
-        i = (int)(f0 - tiles_before(c, g));
+        const Range r = c.range[pair];
+        left = r.n;
+        g = r.g;
+        i = r.i;
         enter_group(c);
-        if (i >= c.pre && left > 0) {
+        if (i >= c.pre) {
             const int k = i - c.pre;
-            s = seq0 + k / (c.own + c.win);
+            s += k / (c.own + c.win);
             w = k % (c.own + c.win);
             enter_sequence(c);
         }
     }
-    __device__ __forceinline__ bool next(const PairArgs& c, Tile& t) {
-        if (!fresh && i < c.pre && left > 0) {  // the common step: from one prefix tile to the next
-            t.kind = kPrefix;
-            t.group = g;
-            t.first = false;
-            t.b = 0;
-            t.y = i * kKeys;
-            t.p0 = t.y;
-            t.n = ++i == c.pre ? c.pre_tail : kKeys;
-            --left;
-            if (i == c.pre && i < per) enter_sequence(c);
-            return true;
-        }
-        return next_any(c, t);
-    }
-    __device__ bool next_any(const PairArgs& c, Tile& t) {
+    __device__ bool next(const PairArgs& c, Tile& t) {
         while (left > 0) {
             if (i == per) {
                 ++g;
@@ -169,13 +159,14 @@ struct Walk {
                 if (c.pre == 0) enter_sequence(c);
             }
             --left;
-            bool live = true;
+            bool live = true, same = false;
             if (i < c.pre) {
                 t.kind = kPrefix;
                 t.y = i * kKeys;
                 t.n = i + 1 == c.pre ? c.pre_tail : kKeys;
                 t.b = 0;
                 t.p0 = t.y;
+                same = !fresh && t.n == kKeys;  // every tile before it in its piece was one
                 if (++i == c.pre && i < per) enter_sequence(c);
             } else {
                 t.b = s;
@@ -209,7 +200,7 @@ struct Walk {
             }
             if (live) {
                 t.group = g;
-                t.first = fresh;
+                t.flags = (fresh ? kFirst : 0) | (same ? kSame : 0);
                 fresh = false;
                 return true;
             }
@@ -226,41 +217,41 @@ __device__ void fault(Smem& sm, const PairArgs& c, uint32_t rank) {
 __device__ __forceinline__ bool aborted(Smem& sm) { return *reinterpret_cast<volatile int*>(&sm.abort_flag) != 0; }
 
 // ---------------------------------------------------------------------
-// warp 0, one lane: queries and this CTA's 32 keys of every tile.  Both CTAs' copies complete on CTA 0's
-// barriers, which expect the bytes of both.
+// warp 0, one lane: finds the tiles, tells the other warps of this CTA about them, and loads the queries and this CTA's
+// 32 keys.  Both CTAs' copies complete on CTA 0's barriers, which expect the bytes of both.
 // ---------------------------------------------------------------------
 struct Maps {
-    CUtensorMap x[3], z[3], q;  // by Kind: 32 rows x 8 slabs; 32 rows x 1 slab
+    CUtensorMap x[3], z[3], q;  // by Kind: 64 rows x 8 slabs; 64 rows x 1 slab
 };
 
 __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal(), once = tc::l2_stream_policy((int)((c.per_seq + kRows - 1) / kRows));
+    const uint32_t x_full = tc::peer_addr(&sm.x_full[0], 0), q_full = tc::peer_addr(&sm.q_full, 0);
     Walk walk(c, pair);
     Tile t, nxt;
     int j = 0, piece = 0;
     bool ok = true, more = walk.next(c, t);
-    if (!more && rank == 0) {
-        sm.flags[0] = kNone;
-        tc::mbar_arrive(&sm.x_full[0]);
+    if (!more) {
+        sm.tile[0].flags = kNone;
+        tc::mbar_arrive(&sm.told[0]);
+        if (rank == 0) tc::mbar_arrive(&sm.x_full[0]);
     }
-    for (; more; t = nxt) {
+    for (; more; t = nxt, ++j) {
+        const int st = j % kStages;
         if (aborted(sm)) { ok = false; break; }
-        if (t.first) {
+        if (t.flags & kFirst) {
             if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1)) { ok = false; break; }
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
-            tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, tc::peer_addr(&sm.q_full, 0), again);
+            tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
             ++piece;
         }
-        const int st = j % kStages;
         if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st], (j / kStages - 1) & 1)) { ok = false; break; }
         more = walk.next(c, nxt);
-        if (rank == 0) {
-            sm.flags[st] = (t.first ? kFirst : 0u) | (!more || nxt.first ? kLast : 0u) | (more ? 0u : kEnd);
-            tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
-        }
-        tc::tma_load_4d_pair(sm.kv[st], &maps.x[t.kind], 0, t.y + (int)rank * 32, 0, t.b, tc::peer_addr(&sm.x_full[st], 0),
-                             t.kind == kPrefix ? again : once);
-        ++j;
+        t.flags |= !more ? kLast | kEnd : nxt.flags & kFirst ? kLast : 0;
+        sm.tile[st] = t;
+        tc::mbar_arrive(&sm.told[st]);
+        if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
+        tc::tma_load_4d_pair(sm.kv[st], &maps.x[t.kind], 0, t.y + (int)rank * kOwnKeys, 0, t.b, x_full + 8 * st, t.kind == kPrefix ? again : once);
     }
     if (!ok) {  // what was asked for lands long before this ends
         fault(sm, c, rank);
@@ -269,38 +260,38 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
 }
 
 // warp 10, one lane: the other CTA's 32 keys of this CTA's slabs, once S has been computed
-__device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
+__device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal();
     const uint32_t other = rank ^ 1;
-    Walk walk(c, pair);
-    Tile t;
-    for (int j = 0; walk.next(c, t); ++j) {
+    for (int j = 0;; ++j) {
         const int st = j % kStages;
-        if (aborted(sm) || !tc::mbar_wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) {
-            fault(sm, c, rank);
-            break;
-        }
+        const uint32_t phase = (j / kStages) & 1;
+        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase)) { fault(sm, c, rank); return; }
+        const Tile t = sm.tile[st];
+        if (t.flags & kNone) return;
+        if (!tc::mbar_wait(&sm.s_full[st], phase)) { fault(sm, c, rank); return; }
         tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
 #pragma unroll 1
         for (int u = 0; u < 4; ++u)
-            tc::tma_load_4d(sm.kv[st] + 8192 * u + 4096 * other, &maps.z[t.kind], 0, t.y + (int)other * 32, 2 * u + (int)rank, t.b,
+            tc::tma_load_4d(sm.kv[st] + kSlab * (2 * u + other), &maps.z[t.kind], 0, t.y + (int)other * kOwnKeys, 2 * u + (int)rank, t.b,
                             &sm.z_full[st], again);
+        if (t.flags & kEnd) return;
     }
 }
 
 // warp 1 of CTA 1, one lane: tells CTA 0 that Z has landed here
-__device__ void pass_on_z(Smem& sm, const PairArgs& c, int pair) {
+__device__ void pass_on_z(Smem& sm, const PairArgs& c) {
     const uint32_t ready = tc::peer_addr(&sm.z_ready[0], 0);
-    Walk walk(c, pair);
-    Tile t;
-    for (int j = 0; walk.next(c, t); ++j) {
+    for (int j = 0;; ++j) {
         const int st = j % kStages;
-        if (aborted(sm) || !tc::mbar_wait(&sm.z_full[st], (j / kStages) & 1)) {
-            fault(sm, c, 1);
-            break;
-        }
+        const uint32_t phase = (j / kStages) & 1;
+        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase)) { fault(sm, c, 1); return; }
+        const int flags = sm.tile[st].flags;
+        if (flags & kNone) return;
+        if (!tc::mbar_wait(&sm.z_full[st], phase)) { fault(sm, c, 1); return; }
         tc::fence_proxy_async();
         tc::peer_arrive(ready + 8 * st);
+        if (flags & kEnd) return;
     }
 }
 
@@ -310,66 +301,74 @@ __device__ void pass_on_z(Smem& sm, const PairArgs& c, int pair) {
 // instructions fetched again costs more than an MMA (all 40 of a tile unrolled, a copy per stage, took 75 cycles
 // each to issue, rolled 44; the smaller ones execute in 26).
 // ---------------------------------------------------------------------
-__device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+// Descriptors: the address, in 16-byte units, is in the low word and the rest of the high one the same for all.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kAll = 0xffffffffu;
+
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-    bool ok = false;
-    for (uint32_t i = 0; i < tc::kWaitPolls && !ok; ++i) ok = tc::mbar_try_cluster(bar, parity);
-    return __all_sync(0xffffffffu, ok);
+    for (uint32_t i = 0; i < tc::kWaitPolls; ++i)
+        if (__any_sync(kAll, tc::mbar_try_cluster(bar, parity))) return true;
+    return false;
 }
 
-// S = Q K^T: A = Q (64 rows per CTA), B = 32 keys per CTA
+// S = Q K^T: A = Q (64 rows per CTA), B = 64 keys per CTA.  One S buffer per stage: a stage that is free again means
+// that its S was read.
 __device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
-    static_assert(kStages == kSBufs, "one S buffer per stage: a stage that is free again means that its S was read");
-    const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024), b0 = tc::sw128_desc(tc::smem_u32(sm.kv), 16, 1024);
+    const uint32_t a0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024), b0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.kv), 16, 1024);
     int pieces = 0;
-    bool ok = true;
-    for (int j = 0;; ++j) {
-        const int st = j % kStages;
-        ok = wait_cluster(&sm.x_full[st], (uint32_t)(j / kStages) & 1);
-        if (!ok) break;
-        const uint32_t flags = __shfl_sync(0xffffffffu, sm.flags[st], 0);
-        if (flags & kNone) break;
+    bool ok = wait_cluster(&sm.x_full[0], 0);
+    int flags = ok ? sm.tile[0].flags : kNone;
+    for (int j = 0; ok && !(flags & kNone); ++j) {
+        const int st = j % kStages, st1 = (j + 1) % kStages;
+        const uint32_t phase1 = (uint32_t)((j + 1) / kStages) & 1;
         if (flags & kFirst) ok = wait_cluster(&sm.q_full, pieces++ & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        uint64_t a = a0, b = dadd(b0, st * kXBytes);
+        uint32_t a = a0, b = b0 + st * (kXBytes >> 4);
         const uint32_t d = tmem + kColS + kColsS * st;
 #pragma unroll 1
         for (int s = 0; s < 8; ++s) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc::mma_f16_pair(d, dadd(a, kk * 32), dadd(b, kk * 32), kIdescQK, (uint32_t)(s | kk));
-            a = dadd(a, 8192);
-            b = dadd(b, 4096);
+            for (int kk = 0; kk < 4; ++kk) tc::mma_f16_pair(d, a + 2 * kk, b + 2 * kk, kDescHigh, kIdescQK, (uint32_t)(s | kk));
+            a += kSlab >> 4;  // a slab of 64 rows of Q is as large
+            b += kSlab >> 4;
         }
         tc::mma_commit_pair(&sm.s_full[st]);
         if (flags & kLast) tc::mma_commit_pair(&sm.q_empty);
         if (flags & kEnd) break;
+        ok = wait_cluster(&sm.x_full[st1], phase1);
+        flags = sm.tile[st1].flags;
     }
     if (!ok) fault(sm, c, 0);
     tc::mma_commit_pair(&sm.drain);
 }
-// O += P V: A = P (64 rows of 128 bytes per CTA), B = 16 keys x 128 dims (2 slabs, 8 KB apart) per CTA
-__device__ void issue_o(Smem& sm, const PairArgs& c, uint32_t tmem, int pair) {
-    const uint64_t a0 = tc::sw128_desc(tc::smem_u32(sm.p), 16, 1024), b0 = tc::sw128_desc(tc::smem_u32(sm.kv), 8192, 1024);
-    Walk walk(c, pair);
-    Tile t;
+// O += P V: A = P (64 rows of 128 bytes per CTA and half of the keys), B = 16 keys x 128 dims (2 blocks, 16 KB apart) per
+// CTA
+__device__ void issue_o(Smem& sm, const PairArgs& c, uint32_t tmem) {
+    const uint32_t a0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.p), 16, 1024), b0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.kv), 2 * kSlab, 1024);
     bool ok = true;
-    for (int j = 0; __any_sync(0xffffffffu, walk.next(c, t)); ++j) {
+    for (int j = 0;; ++j) {
         const int st = j % kStages;
-        const uint32_t phase = (uint32_t)(j / kStages) & 1, fresh = __any_sync(0xffffffffu, t.first);
-        ok = wait_cluster(&sm.z_full[st], phase) && wait_cluster(&sm.z_ready[st], phase) && wait_cluster(&sm.p_full[j & 1], (uint32_t)(j >> 1) & 1);
+        const uint32_t phase = (uint32_t)(j / kStages) & 1;
+        ok = wait_cluster(&sm.told[st], phase);
+        if (!ok) break;
+        const int flags = sm.tile[st].flags;
+        if (flags & kNone) break;
+        ok = wait_cluster(&sm.z_full[st], phase) && wait_cluster(&sm.z_ready[st], phase) && wait_cluster(&sm.p_full, (uint32_t)j & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        uint64_t a = dadd(a0, (j & 1) * (kHalf * 128)), b = dadd(b0, st * kXBytes);
+        uint32_t a = a0, b = b0 + st * (kXBytes >> 4);
+        const uint32_t add = flags & kFirst ? 0 : 1;
 #pragma unroll 1
         for (int kk = 0; kk < kKeys / 16; ++kk) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) tc::mma_f16_pair(tmem + 128 * h, a, dadd(b, 16384 * h), kIdescPV, (uint32_t)kk | (fresh ^ 1));
-            a = dadd(a, 32);
-            b = dadd(b, 2048);
+            for (int h = 0; h < 2; ++h) tc::mma_f16_pair(tmem + 128 * h, a, b + (4 * kSlab >> 4) * h, kDescHigh, kIdescPV, (uint32_t)kk | add);
+            a += kk == 3 ? (kHalf * 128 - 96) >> 4 : 32 >> 4;
+            b += 2048 >> 4;
         }
         tc::mma_commit_pair(&sm.kv_empty[st]);
-        tc::mma_commit_pair(&sm.p_free[j & 1]);
+        tc::mma_commit_pair(&sm.p_free);
+        if (flags & kEnd) break;
     }
     if (!ok) fault(sm, c, 0);
     tc::mma_commit_pair(&sm.drain);
@@ -396,32 +395,39 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results below t
 __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, uint32_t rank) {
     const SharedArgs& a = c.a;
     // TMEM lanes 32 sub ..: rows 32 (sub & 1) .., of a tile's keys (and of O's slabs) half sub >> 1; the second
-    // four warps take the second 16 of those keys.  So four threads share a row, each a quarter of the keys.
+    // four warps take the second 32 of those keys.  So four threads share a row, each a quarter of the keys.
     const int sub = (threadIdx.x >> 5) & 3, wg = (threadIdx.x - 64) >> 7;
     const int lane = threadIdx.x & 31, half = sub >> 1, r = 32 * (sub & 1) + lane, quarter = 2 * half + wg;
-    const int key0 = 16 * quarter;
-    const int bar = 1 + (sub & 1);  // the four warps that share rows
+    const int key0 = 32 * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
-    const uint32_t p_full0 = tc::peer_addr(&sm.p_full[0], 0);
-    uint8_t* const prow = sm.p[0] + (r >> 3) * 1024 + (r & 7) * 128;
-    const uint32_t chunk0 = ((2 * quarter) ^ (r & 7)) << 4, chunk1 = ((2 * quarter + 1) ^ (r & 7)) << 4;
-    Walk walk(c, pair);
-    Tile t, nxt;
-    bool more = walk.next(c, t), ok = true;
-    int next_group = c.g0[pair];
+    const uint32_t p_full = tc::peer_addr(&sm.p_full, 0);
+    uint8_t* const prow = sm.p[half] + (r >> 3) * 1024 + (r & 7) * 128;
+    const int first_group = c.range[pair].g, last_group = c.range[pair].last;
+    auto ml = [&](int group) -> float2& { return c.part_ml[(pair + (long long)group) * kRows + rank * kHalf + r]; };
+    int next_group = first_group;
     float m_run = -INFINITY, l_run = 0.f;
     // this row's query
     int b = 0;
     long long pos = 0, seen = 0;
-    bool alive = false;
-    auto wait = [&](uint64_t* bar_, uint32_t parity) {
-        if (ok) ok = tc::mbar_wait(bar_, parity);
-        ok = __all_sync(0xffffffffu, ok);
+    bool alive = false, ok = true;
+    uint32_t mask = 0;  // of this thread's 32 keys
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(kAll, ok && tc::mbar_test(bar, parity))) return true;
+        if (ok) ok = tc::mbar_wait(bar, parity);
+        ok = __all_sync(kAll, ok);
         return ok;
     };
-    // a time-out leaves `ok` false: the rest of the range is walked for its barriers only
-    for (int j = 0; more; ++j) {
-        if (t.first) {
+    // a time-out makes `ok` false, which the barrier of the (next) tile tells all eight warps: they leave together
+    for (int j = 0;; ++j) {
+        const int st = j % kStages;
+        const uint32_t phase = (j / kStages) & 1;
+        Tile t;
+        t.flags = kSame;
+        t.kind = kPrefix;
+        t.group = first_group;
+        if (wait(&sm.told[st], phase)) t = sm.tile[st];
+        if (t.flags & kNone) break;
+        if (t.flags & kFirst) {
             m_run = -INFINITY;
             l_run = 0.f;
             const unsigned row = (unsigned)t.group * kRows + rank * kHalf + r;
@@ -434,9 +440,8 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 seen = seen_entries(a, pos);
             }
         }
-        // this thread's 16 keys
-        uint32_t mask = alive ? 0xffffu : 0u;
-        if (t.kind != kPrefix || t.n < kKeys) {
+        if (!(t.flags & kSame)) {
+            mask = alive ? ~0u : 0u;
             const int n = t.n - key0;
             if (t.kind == kPrefix) {
                 mask &= low_bits(n);
@@ -444,11 +449,11 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 const bool mine = alive && b == t.b;
                 if (a.own_entry) {
                     int e = -1;
-                    if (lane < 16 && lane < n) e = a.own_entry[(long long)t.b * a.own_rows + t.p0 + key0 + lane];
+                    if (lane < n) e = a.own_entry[(long long)t.b * a.own_rows + t.p0 + key0 + lane];
                     mask = 0;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int ek = __shfl_sync(0xffffffffu, e, k);
+#pragma unroll 4
+                    for (int k = 0; k < 32; ++k) {
+                        const int ek = __shfl_sync(kAll, e, k);
                         mask |= (uint32_t)(ek >= 0 && ek < seen) << k;
                     }
                     if (!mine) mask = 0;
@@ -461,36 +466,41 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 mask = alive && b == t.b ? mask & low_bits(to < n ? to : n) & ~low_bits(from) : 0u;
             }
         }
-        float x[16];
-        if (wait(&sm.s_full[j % kSBufs], (j / kSBufs) & 1)) {
+        float x[32];
+        if (wait(&sm.s_full[st], phase)) {
             tc::tc_fence_after();
-            uint32_t u[16];
-            tc::tmem_ld_x16(lanes + kColS + kColsS * (j % kSBufs) + 16 * wg, u);
+            uint32_t u[32];
+            tc::tmem_ld_x32(lanes + kColS + kColsS * st + 32 * wg, u);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(u[k]);
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(u[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
+            for (int k = 0; k < 32; ++k) x[k] = 0.f;
         }
         bool odd = false;  // a key of this tile is not finite
         if (t.kind != kPrefix) {
             float d = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) d = fmaf(x[k], 0.f, d);
+            for (int k = 0; k < 32; ++k) d = fmaf(x[k], 0.f, d);
             odd = !(d == 0.f);
         }
-        if (mask != 0xffffu) {
+        if (mask != ~0u) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = (mask >> k) & 1 ? x[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) x[k] = (mask >> k) & 1 ? x[k] : -INFINITY;
         }
         float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int k = 4; k < 16; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
-        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));  // of four NaN: NaN
+        for (int k = 4; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
+        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));  // of NaN alone: NaN
         sm.mx[j & 1][quarter][r] = mt;
-        if (t.kind == kPrefix) tc::named_barrier(bar, 128);
-        else odd = tc::named_barrier_or(3, 256, odd);
+        if (tc::named_barrier_or(1, 256, odd || !ok)) {
+            if (tc::named_barrier_or(1, 256, !ok)) {
+                ok = false;
+                break;
+            }
+            odd = true;
+        }
         mt = fmaxf(fmaxf(sm.mx[j & 1][0][r], sm.mx[j & 1][1][r]), fmaxf(sm.mx[j & 1][2][r], sm.mx[j & 1][3][r])) * c.scale_log2;
         float alpha = 1.f;
         if (mt > m_run + kSlack) {
@@ -499,18 +509,20 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         }
         l_run *= alpha;
         const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
-        uint32_t pk[8];
+        uint32_t pk[16];
         float ls[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
             const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
             ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
             const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
             pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
         }
         l_run += ls[0] + ls[1];
-        if (__any_sync(0xffffffffu, alpha != 1.f) && wait(&sm.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
-            // O, complete up to the tile before, follows the maximum: 128 columns of this warp's lanes
+        // P and O are free once the product of the tile before is done
+        const bool free = j == 0 || wait(&sm.p_free, (j - 1) & 1);
+        if (__any_sync(kAll, alpha != 1.f) && free) {
+            // O follows the maximum: 128 columns of this warp's lanes
             tc::tc_fence_after();
 #pragma unroll 1
             for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
@@ -523,15 +535,15 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
             }
             tc::tmem_st_wait();
         }
-        // the P buffer of this parity is free once the product two tiles back is done
-        if (j < 2 || wait(&sm.p_free[j & 1], ((j >> 1) - 1) & 1)) {
-            uint8_t* pr = prow + (j & 1) * (kHalf * 128);
-            *reinterpret_cast<uint4*>(pr + chunk0) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4*>(pr + chunk1) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        if (free) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(prow + (((4 * wg + k) ^ (r & 7)) << 4)) =
+                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
-        if (odd && wait(&sm.z_full[j % kStages], (j / kStages) & 1)) {
+        if (odd && wait(&sm.z_full[st], phase)) {
             // both halves of V are here: scrub it
-            uint4* v = reinterpret_cast<uint4*>(sm.kv[j % kStages]);
+            uint4* v = reinterpret_cast<uint4*>(sm.kv[st]);
             for (int k = threadIdx.x - 64; k < (int)(kXBytes / 16); k += 256) {
                 const uint4 w = v[k];
                 v[k] = make_uint4(scrub(w.x), scrub(w.y), scrub(w.z), scrub(w.w));
@@ -540,24 +552,22 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         tc::fence_proxy_async();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) tc::peer_arrive(p_full0 + 8 * (j & 1));
+        if (lane == 0 && ok) tc::peer_arrive(p_full);
 
-        more = walk.next(c, nxt);
-        if (!more || nxt.first) {
+        if (t.flags & kLast) {
             // write the piece
-            const long long piece = pair + t.group;
             for (; next_group < t.group; ++next_group)  // groups of the range without a tile that holds anything
-                if (quarter == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
-            next_group = t.group + 1;
+                if (quarter == 0) ml(next_group) = make_float2(-INFINITY, 0.f);
+            ++next_group;
             sm.ls[quarter][r] = l_run;
-            tc::named_barrier(bar, 128);
+            tc::named_barrier(1, 256);
             if (quarter == 0) {
                 const float l = (l_run + sm.ls[1][r]) + (sm.ls[2][r] + sm.ls[3][r]);
-                c.part_ml[piece * kRows + rank * kHalf + r] = make_float2(isnan(l) ? NAN : m_run, l);
+                ml(t.group) = make_float2(isnan(l) ? NAN : m_run, l);
             }
-            if (wait(&sm.p_free[j & 1], (j >> 1) & 1)) {
+            if (wait(&sm.p_free, j & 1)) {
                 tc::tc_fence_after();
-                float4* po = c.part_o + piece * (kRows * kD / 4) + rank * kHalf + r;
+                float4* po = c.part_o + (pair + (long long)t.group) * (kRows * kD / 4) + rank * kHalf + r;
 #pragma unroll 1
                 for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
                     uint32_t o[32];
@@ -573,15 +583,14 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 tc::tc_fence_before();
             }
         }
-        t = nxt;
+        if (t.flags & kEnd) break;
     }
-    const long long f1 = range_start(c, pair + 1);
-    for (; next_group < c.groups && tiles_before(c, next_group) < f1; ++next_group)
-        if (quarter == 0) c.part_ml[(pair + (long long)next_group) * kRows + rank * kHalf + r] = make_float2(-INFINITY, 0.f);
+    for (; next_group <= last_group; ++next_group)
+        if (quarter == 0) ml(next_group) = make_float2(-INFINITY, 0.f);
     if (!ok || aborted(sm)) {
         fault(sm, c, rank);
-        for (int g = c.g0[pair]; g < next_group; ++g)
-            if (quarter == 0) c.part_ml[(pair + (long long)g) * kRows + rank * kHalf + r] = make_float2(NAN, NAN);
+        for (int g = first_group; g <= last_group; ++g)
+            if (quarter == 0) ml(g) = make_float2(NAN, NAN);
     }
 }
 
@@ -593,16 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const int pair = blockIdx.x >> 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&sm.told[i], 1);
             tc::mbar_init(&sm.x_full[i], 1);
             tc::mbar_init(&sm.z_full[i], 1);
             tc::mbar_init(&sm.z_ready[i], 1);
             tc::mbar_init(&sm.kv_empty[i], 1);
+            tc::mbar_init(&sm.s_full[i], 1);
         }
-        for (int i = 0; i < kSBufs; ++i) tc::mbar_init(&sm.s_full[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sm.p_full[i], 16);  // the softmax warps of both CTAs
-            tc::mbar_init(&sm.p_free[i], 1);
-        }
+        tc::mbar_init(&sm.p_full, 16);  // the softmax warps of both CTAs
+        tc::mbar_init(&sm.p_free, 1);
         tc::mbar_init(&sm.q_full, 1);
         tc::mbar_init(&sm.q_empty, 1);
         tc::mbar_init(&sm.drain, 2);  // both warps that issue
@@ -619,12 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (warp == 0) {
         if (lane == 0) load_x(sm, c, maps, pair, rank);
     } else if (warp == 10) {
-        if (lane == 0) load_z(sm, c, maps, pair, rank);
+        if (lane == 0) load_z(sm, c, maps, rank);
     } else if (warp == 1) {
         if (rank == 0) issue_s(sm, c, tmem);
-        else if (lane == 0) pass_on_z(sm, c, pair);
+        else if (lane == 0) pass_on_z(sm, c);
     } else if (warp == 11) {
-        if (rank == 0) issue_o(sm, c, tmem, pair);
+        if (rank == 0) issue_o(sm, c, tmem);
     } else {
         softmax(sm, c, tmem, pair, rank);
     }
@@ -661,47 +669,56 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
         live = has_candidates(a, pos);
         if (blockIdx.y == 0 && warp == 0 && h == 0 && query % (unsigned)a.n_q == 0) report_sequence(a, b);
     }
-    // pieces of this group: pairs p0 .. p0 + n - 1
+    // pieces of this group: pairs p0 .. p1, the last ones that begin no later than its first, and its last, tile
     int p0 = 0, n = 0;
-    if (c.total > 0) {
-        const long long f0 = tiles_before(c, g), f1 = tiles_before(c, g + 1);
-        p0 = (int)(((f0 + 1) * c.pairs - 1) / c.total);
-        n = (int)((f1 * c.pairs - 1) / c.total) - p0 + 1;
+    if (c.pairs > 0) {
+        int p1 = 0;
+        for (int k = 64; k > 0; k >>= 1) {
+            if (p0 + k < c.pairs && (c.range[p0 + k].g < g || (c.range[p0 + k].g == g && c.range[p0 + k].i == 0))) p0 += k;
+            if (p1 + k < c.pairs && c.range[p1 + k].g <= g) p1 += k;
+        }
+        n = p1 - p0 + 1;
     }
     const float2* ml = c.part_ml + (long long)(p0 + g) * kRows + rg;
     const float4* po = c.part_o + (long long)(p0 + g) * (kRows * kD / 4) + quad * kRows + rg;
-    float m = -INFINITY;
-    if (live)
-        for (int i = 0; i < n; ++i) {
-            const float x = ml[(long long)i * kRows].x;
-            m = isnan(x) || isnan(m) ? NAN : fmaxf(m, x);
-        }
-    float l = 0.f;
+    // kU pieces are on their way together, their maxima and sums beside them
+    constexpr int kU = 8;
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
-        constexpr int kU = 4;  // pieces in flight
-        for (int i0 = 0; i0 < n; i0 += kU) {
-            float4 v[kU];
-            float2 x[kU];
+#pragma unroll 1
+    for (int i0 = 0; live && i0 < n; i0 += kU) {
+        float4 v[kU];
+        float2 x[kU];
+        float top = m;
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (i0 + u >= n) continue;
-                x[u] = ml[(long long)(i0 + u) * kRows];
-                if (x[u].x != -INFINITY) v[u] = __ldcg(po + (long long)(i0 + u) * (kRows * kD / 4));  // else: never written
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (i0 + u >= n || x[u].x == -INFINITY) continue;
-                const float w = exp2f(x[u].x - m);
-                l = fmaf(w, x[u].y, l);
-                o.x = fmaf(w, v[u].x, o.x);
-                o.y = fmaf(w, v[u].y, o.y);
-                o.z = fmaf(w, v[u].z, o.z);
-                o.w = fmaf(w, v[u].w, o.w);
+        for (int u = 0; u < kU; ++u) {
+            x[u] = make_float2(-INFINITY, 0.f);
+            if (i0 + u < n) {
+                x[u] = __ldcg(ml + (long long)(i0 + u) * kRows);
+                v[u] = __ldcg(po + (long long)(i0 + u) * (kRows * kD / 4));  // of a piece without tiles: not used
             }
         }
-        if (a.sink) l += exp2f(a.sink[h] * kLog2eF - m);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) top = isnan(x[u].x) || isnan(top) ? NAN : fmaxf(top, x[u].x);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - top);
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (x[u].x == -INFINITY) continue;
+            const float w = exp2f(x[u].x - top);
+            l = fmaf(w, x[u].y, l);
+            o.x = fmaf(w, v[u].x, o.x);
+            o.y = fmaf(w, v[u].y, o.y);
+            o.z = fmaf(w, v[u].z, o.z);
+            o.w = fmaf(w, v[u].w, o.w);
+        }
+        m = top;
     }
+    if (m != -INFINITY && a.sink) l += exp2f(a.sink[h] * kLog2eF - m);
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
     if (a.lse && blockIdx.y == 0 && warp == 0 && row < c.rows)
         a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
@@ -786,14 +803,19 @@ void plan(const SharedArgs& a, PairArgs* c) {
     c->scale_log2 = kLog2eF / sqrtf((float)kD);
     int g = 0;
     for (int p = 0; p < c->pairs; ++p) {
-        const long long f = (long long)p * c->total / c->pairs;
+        const long long f = (long long)p * c->total / c->pairs, f1 = (long long)(p + 1) * c->total / c->pairs;
         int hi = c->groups;  // the last group that begins at or before tile f
         while (hi - g > 1) {
             const int mid = g + (hi - g) / 2;
             if (tiles_before(*c, mid) <= f) g = mid;
             else hi = mid;
         }
-        c->g0[p] = g;
+        Range& r = c->range[p];
+        r.g = g;
+        r.i = (int)(f - tiles_before(*c, g));
+        r.n = (int)(f1 - f);
+        if (p > 0) c->range[p - 1].last = r.i > 0 ? g : g - 1;
+        r.last = c->groups - 1;
     }
 }
 long long pieces(const PairArgs& c) { return c.total > 0 ? (long long)c.groups + c.pairs - 1 : 0; }
@@ -823,8 +845,8 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
         bool ok = make_map(&maps.q, a.q, 1, c.rows, kHalf, 8);
         for (int k = 0; k < 3; ++k) {
             const bool have = in[k].p && in[k].rows > 0;  // without: no tile asks for it
-            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, 32, 8) &&
-                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, 32, 1);
+            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 8) &&
+                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 1);
         }
         if (!ok) return cudaErrorNotSupported;
         const size_t smem = sizeof(Smem) + 1024;
