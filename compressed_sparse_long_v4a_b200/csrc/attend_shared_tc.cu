@@ -39,6 +39,7 @@
 #include "internal.h"
 #include "shared.h"
 #include "tc.cuh"
+#include "turns.h"
 
 namespace v4a {
 namespace {
@@ -77,7 +78,7 @@ struct __align__(1024) Smem {
     float mx[2][4][kHalf];  // row maxima of a tile's quarters, by tile parity
     float ls[4][kHalf];
     // x_full, z_ready, p_full and q_full count in CTA 0 only
-    uint64_t told[kStages], x_full[kStages], z_full[kStages], z_ready[kStages], kv_empty[kStages], s_full[kStages];
+    uint64_t told[kStages], x_full[kStages][2], z_full[kStages], z_ready[kStages], kv_empty[kStages][2], s_full[kStages];
     uint64_t p_full, p_free;
     uint64_t q_full, q_empty, drain;
     int abort_flag;
@@ -117,7 +118,7 @@ long long tiles_before(const PairArgs& c, int g) {
 struct Walk {
     int left, g, i, per;        // tiles to go; group, tile in it, its tiles
     int s, w;                   // sequence and its tile
-    bool fresh;                 // no tile of this group yet
+    bool fresh, entered;        // no tile of this group yet; the sequence's numbers are read
     int count, row0, n_a, n_w;  // own slots; window: ring row of position lo, positions before the ring's end, all
     long long lo;
 
@@ -126,6 +127,7 @@ struct Walk {
         s = (int)(r0 / c.per_seq);
         per = c.pre + ((int)(r1 / c.per_seq) - s + 1) * (c.own + c.win);
         fresh = true;
+        entered = false;
         w = 0;
     }
     __device__ void enter_sequence(const PairArgs& c) {
@@ -147,7 +149,6 @@ struct Walk {
             const int k = i - c.pre;
             s += k / (c.own + c.win);
             w = k % (c.own + c.win);
-            enter_sequence(c);
         }
     }
     __device__ bool next(const PairArgs& c, Tile& t) {
@@ -156,7 +157,6 @@ struct Walk {
                 ++g;
                 i = 0;
                 enter_group(c);
-                if (c.pre == 0) enter_sequence(c);
             }
             --left;
             bool live = true, same = false;
@@ -167,8 +167,10 @@ struct Walk {
                 t.b = 0;
                 t.p0 = t.y;
                 same = !fresh && t.n == kKeys;  // every tile before it in its piece was one
-                if (++i == c.pre && i < per) enter_sequence(c);
+                ++i;
             } else {
+                if (!entered) enter_sequence(c);
+                entered = true;
                 t.b = s;
                 if (w < c.own) {
                     t.kind = kOwn;
@@ -195,7 +197,7 @@ struct Walk {
                 if (++w == c.own + c.win) {
                     w = 0;
                     ++s;
-                    if (i < per) enter_sequence(c);
+                    entered = false;
                 }
             }
             if (live) {
@@ -221,37 +223,49 @@ __device__ __forceinline__ bool aborted(Smem& sm) { return *reinterpret_cast<vol
 // 32 keys.  Both CTAs' copies complete on CTA 0's barriers, which expect the bytes of both.
 // ---------------------------------------------------------------------
 struct Maps {
-    CUtensorMap x[3], z[3], q;  // by Kind: 64 rows x 8 slabs; 64 rows x 1 slab
+    CUtensorMap x[3], z[3], q;  // by Kind: 64 rows x 4 slabs; 64 rows x 1 slab
 };
 
 __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal(), once = tc::l2_stream_policy((int)((c.per_seq + kRows - 1) / kRows));
-    const uint32_t x_full = tc::peer_addr(&sm.x_full[0], 0), q_full = tc::peer_addr(&sm.q_full, 0);
+    const uint32_t x_full = tc::peer_addr(&sm.x_full[0][0], 0), q_full = tc::peer_addr(&sm.q_full, 0);
     Walk walk(c, pair);
     Tile t, nxt;
     int j = 0, piece = 0;
-    bool ok = true, more = walk.next(c, t);
+    bool ok = true, more = true;
+    // what can be done before the kernel before this one has finished: a prefix tile depends on sizes alone
+    const bool early = c.range[pair].i < c.pre;
+    if (early) walk.next(c, t);
+    griddep_wait();
+    if (!early) more = walk.next(c, t);
     if (!more) {
         sm.tile[0].flags = kNone;
         tc::mbar_arrive(&sm.told[0]);
-        if (rank == 0) tc::mbar_arrive(&sm.x_full[0]);
+        if (rank == 0) tc::mbar_arrive(&sm.x_full[0][0]);
     }
     for (; more; t = nxt, ++j) {
         const int st = j % kStages;
         if (aborted(sm)) { ok = false; break; }
+        more = walk.next(c, nxt);
+        t.flags |= !more ? kLast | kEnd : nxt.flags & kFirst ? kLast : 0;
         if (t.flags & kFirst) {
             if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1)) { ok = false; break; }
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
             tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
             ++piece;
         }
-        if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st], (j / kStages - 1) & 1)) { ok = false; break; }
-        more = walk.next(c, nxt);
-        t.flags |= !more ? kLast | kEnd : nxt.flags & kFirst ? kLast : 0;
-        sm.tile[st] = t;
-        tc::mbar_arrive(&sm.told[st]);
-        if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st], 2 * kXBytes);
-        tc::tma_load_4d_pair(sm.kv[st], &maps.x[t.kind], 0, t.y + (int)rank * kOwnKeys, 0, t.b, x_full + 8 * st, t.kind == kPrefix ? again : once);
+        // slabs 0-3, then 4-7: O is done with them one after the other
+        for (int h = 0; h < 2; ++h) {
+            if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st][h], (j / kStages - 1) & 1)) { ok = false; break; }
+            if (h == 0) {
+                sm.tile[st] = t;
+                tc::mbar_arrive(&sm.told[st]);
+            }
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st][h], kXBytes);
+            tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[t.kind], 0, t.y + (int)rank * kOwnKeys, 4 * h, t.b, x_full + 16 * st + 8 * h,
+                                 t.kind == kPrefix ? again : once);
+        }
+        if (!ok) break;
     }
     if (!ok) {  // what was asked for lands long before this ends
         fault(sm, c, rank);
@@ -316,7 +330,7 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
 __device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
     const uint32_t a0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024), b0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.kv), 16, 1024);
     int pieces = 0;
-    bool ok = wait_cluster(&sm.x_full[0], 0);
+    bool ok = wait_cluster(&sm.x_full[0][0], 0);
     int flags = ok ? sm.tile[0].flags : kNone;
     for (int j = 0; ok && !(flags & kNone); ++j) {
         const int st = j % kStages, st1 = (j + 1) % kStages;
@@ -328,15 +342,18 @@ __device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
         const uint32_t d = tmem + kColS + kColsS * st;
 #pragma unroll 1
         for (int s = 0; s < 8; ++s) {
+            if (s == 4 && !wait_cluster(&sm.x_full[st][1], (uint32_t)(j / kStages) & 1)) ok = false;
+            if (s == 4) tc::tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) tc::mma_f16_pair(d, a + 2 * kk, b + 2 * kk, kDescHigh, kIdescQK, (uint32_t)(s | kk));
             a += kSlab >> 4;  // a slab of 64 rows of Q is as large
             b += kSlab >> 4;
         }
+        if (!ok) break;
         tc::mma_commit_pair(&sm.s_full[st]);
         if (flags & kLast) tc::mma_commit_pair(&sm.q_empty);
         if (flags & kEnd) break;
-        ok = wait_cluster(&sm.x_full[st1], phase1);
+        ok = wait_cluster(&sm.x_full[st1][0], phase1);
         flags = sm.tile[st1].flags;
     }
     if (!ok) fault(sm, c, 0);
@@ -357,16 +374,22 @@ __device__ void issue_o(Smem& sm, const PairArgs& c, uint32_t tmem) {
         ok = wait_cluster(&sm.z_full[st], phase) && wait_cluster(&sm.z_ready[st], phase) && wait_cluster(&sm.p_full, (uint32_t)j & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        uint32_t a = a0, b = b0 + st * (kXBytes >> 4);
+        uint32_t b = b0 + st * (kXBytes >> 4);
         const uint32_t add = flags & kFirst ? 0 : 1;
 #pragma unroll 1
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
+        for (int h = 0; h < 2; ++h) {  // 256 dims
+            uint32_t a = a0;
+#pragma unroll 1
+            for (int kk = 0; kk < kKeys / 16; kk += 4) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) tc::mma_f16_pair(tmem + 128 * h, a, b + (4 * kSlab >> 4) * h, kDescHigh, kIdescPV, (uint32_t)kk | add);
-            a += kk == 3 ? (kHalf * 128 - 96) >> 4 : 32 >> 4;
-            b += 2048 >> 4;
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_f16_pair(tmem + 128 * h, a + 2 * k, b + (2048 >> 4) * k, kDescHigh, kIdescPV, (uint32_t)(kk | k) | add);
+                a += kHalf * 128 >> 4;
+                b += 4 * 2048 >> 4;
+            }
+            b += 2 * kSlab >> 4;
+            tc::mma_commit_pair(&sm.kv_empty[st][h]);
         }
-        tc::mma_commit_pair(&sm.kv_empty[st]);
         tc::mma_commit_pair(&sm.p_free);
         if (flags & kEnd) break;
     }
@@ -603,10 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sm.told[i], 1);
-            tc::mbar_init(&sm.x_full[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                tc::mbar_init(&sm.x_full[i][h], 1);
+                tc::mbar_init(&sm.kv_empty[i][h], 1);
+            }
             tc::mbar_init(&sm.z_full[i], 1);
             tc::mbar_init(&sm.z_ready[i], 1);
-            tc::mbar_init(&sm.kv_empty[i], 1);
             tc::mbar_init(&sm.s_full[i], 1);
         }
         tc::mbar_init(&sm.p_full, 16);  // the softmax warps of both CTAs
@@ -622,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     __syncthreads();
     tc::cluster_sync();
     tc::tc_fence_after();
-    griddep_wait();  // everything before this kernel on the stream has finished
+    if (warp > 0) griddep_wait();  // everything before this kernel on the stream has finished (warp 0: see load_x)
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0) {
         if (lane == 0) load_x(sm, c, maps, pair, rank);
@@ -649,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 
 // Joins the pieces.  A block takes 32 rows (a lane each) and 16 dims (4 per warp): a warp's load of a
 // piece is 512 contiguous bytes.  The output leaves through shared memory, 32 or 64 bytes per row.
-__global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_constant__ PairArgs c) {
+__global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_constant__ PairArgs c, const __grid_constant__ Turns turns) {
     griddep_wait();
     griddep_launch_dependents();
     __shared__ float tile[32][20];
@@ -726,21 +751,18 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
     o.y *= inv;
     o.z *= inv;
     o.w *= inv;
-    const int r0 = kD - a.rope_dims;
-    if (a.rope_dims > 0 && live) {
-        float s, co;
-        if (dim >= r0) {
-            rope_sincos(pos, (dim - r0) >> 1, a.rope_dims, a.rope_base, &s, &co);
+    const int k0 = (dim - (kD - a.rope_dims)) >> 1;  // rotated back by the query's position
+    if (live && a.rope_dims > 0 && k0 >= -1) {
+        if (k0 >= 0) {
+            const float2 w = turn((double)pos, turns.hi[k0], turns.lo[k0]);
             const float u = o.x;
-            o.x = fmaf(u, co, -o.y * s);
-            o.y = fmaf(u, s, o.y * co);
+            o.x = fmaf(u, w.x, o.y * w.y);
+            o.y = fmaf(o.y, w.x, -u * w.y);
         }
-        if (dim + 2 >= r0) {
-            rope_sincos(pos, (dim + 2 - r0) >> 1, a.rope_dims, a.rope_base, &s, &co);
-            const float u = o.z;
-            o.z = fmaf(u, co, -o.w * s);
-            o.w = fmaf(u, s, o.w * co);
-        }
+        const float2 w = turn((double)pos, turns.hi[k0 + 1], turns.lo[k0 + 1]);
+        const float u = o.z;
+        o.z = fmaf(u, w.x, o.w * w.y);
+        o.w = fmaf(o.w, w.x, -u * w.y);
     }
     *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = o;
     __syncthreads();
@@ -801,22 +823,44 @@ void plan(const SharedArgs& a, PairArgs* c) {
     c->total = tiles_before(*c, c->groups);
     c->pairs = c->total < kPairs ? (int)c->total : kPairs;
     c->scale_log2 = kLog2eF / sqrtf((float)kD);
-    int g = 0;
-    for (int p = 0; p < c->pairs; ++p) {
-        const long long f = (long long)p * c->total / c->pairs, f1 = (long long)(p + 1) * c->total / c->pairs;
-        int hi = c->groups;  // the last group that begins at or before tile f
-        while (hi - g > 1) {
-            const int mid = g + (hi - g) / 2;
-            if (tiles_before(*c, mid) <= f) g = mid;
-            else hi = mid;
+    // Equal shares of the work: the tiles, and kPiece for every piece (queries loaded, O written).  With many groups
+    // a pair has many pieces anyway, and the tiles alone are shared out.
+    constexpr int kPiece = 2;
+    const int extra = c->groups <= 8 * kPairs ? kPiece : 0;
+    const long long cost = c->total + (long long)extra * (c->groups + c->pairs - 1);
+    long long f = 0;
+    int g = 0, pairs = 0;
+    for (int p = 0; p < c->pairs && f < c->total; ++p) {
+        // up to where the work so far is p + 1 shares
+        long long f1 = f, budget = (p + 1) * cost / c->pairs - (f + (long long)extra * (g + p));
+        int h = g;
+        if (extra == 0) {
+            f1 = (p + 1) * c->total / c->pairs;
+        } else {
+            for (budget -= extra; budget > 0 && f1 < c->total;) {
+                const long long end = tiles_before(*c, h + 1), n = end - f1 < budget ? end - f1 : budget;
+                f1 += n;
+                budget -= n;
+                if (f1 == end) {
+                    ++h;
+                    budget -= extra;
+                }
+            }
+            if (f1 == f) f1 = f + 1;
+            if (p == c->pairs - 1) f1 = c->total;
         }
+        while (g + 1 < c->groups && tiles_before(*c, g + 1) <= f) ++g;
         Range& r = c->range[p];
         r.g = g;
         r.i = (int)(f - tiles_before(*c, g));
         r.n = (int)(f1 - f);
         if (p > 0) c->range[p - 1].last = r.i > 0 ? g : g - 1;
         r.last = c->groups - 1;
+        f = f1;
+        while (g + 1 < c->groups && tiles_before(*c, g + 1) <= f) ++g;
+        pairs = p + 1;
     }
+    c->pairs = pairs;
 }
 long long pieces(const PairArgs& c) { return c.total > 0 ? (long long)c.groups + c.pairs - 1 : 0; }
 
@@ -845,7 +889,7 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
         bool ok = make_map(&maps.q, a.q, 1, c.rows, kHalf, 8);
         for (int k = 0; k < 3; ++k) {
             const bool have = in[k].p && in[k].rows > 0;  // without: no tile asks for it
-            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 8) &&
+            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 4) &&
                  make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 1);
         }
         if (!ok) return cudaErrorNotSupported;
@@ -855,7 +899,9 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
         if (e == cudaSuccess) e = launch_pdl_cluster(shared_tc_kernel, dim3(2 * c.pairs), dim3(kThreads), smem, st, 2, maps, c);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_pdl(shared_tc_join_kernel, dim3((c.rows + 31) / 32, kD / 16), dim3(128), 0, st, c);
+    Turns turns;
+    if (a.rope_dims > 0) make_turns(a.rope_dims, a.rope_base, &turns, [](long double f) { return f; });
+    cudaError_t e = launch_pdl(shared_tc_join_kernel, dim3((c.rows + 31) / 32, kD / 16), dim3(128), 0, st, c, turns);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

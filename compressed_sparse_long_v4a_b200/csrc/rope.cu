@@ -7,16 +7,14 @@
 // copied columns pass through as they are, and no index is worked out per item.  A block takes one
 // token, or several where their rows are few; its (cos, sin) are made once in shared memory while
 // the first rows are on their way.  With few tokens (a decode step) a token's heads are cut over blocks.
-#include <math.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "turns.h"
 
 namespace v4a {
 namespace {
 
 constexpr int kMaxStreams = 8;
-constexpr int kMaxPairs = 256;
 constexpr int kThreads = 256;
 constexpr int kTable = kThreads;  // angles of a block's tokens at most: one per thread
 
@@ -34,25 +32,13 @@ struct RopeStream {
 
 struct RopeArgs {
     RopeStream s[kMaxStreams];
-    double f_hi[kMaxPairs];  // turns (not radians) per position, as a sum of two
-    float f_lo[kMaxPairs];
+    Turns f;
     int n, n_tok, pairs, half, inverse;
     unsigned all_tok;        // batch * n_tok
     float scale;
     const int64_t* positions;
     long long pos_stride, pos0, pos_step;
 };
-
-// cos and sin of p f, f = f_hi + f_lo turns per position: the product as an exact sum of two doubles, so
-// the fraction of a turn keeps more than 24 bits for |p| up to 2^40
-__device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
-    const double hi = p * f_hi;
-    const double lo = fma(p, f_hi, -hi) + p * (double)f_lo;
-    const double frac = (hi - rint(hi)) + lo;
-    float s, c;
-    sincospif((float)(2.0 * frac), &s, &c);
-    return make_float2(c, s);
-}
 
 // a parameter by its address: the lanes of a warp read neighbouring ones, which constant memory serialises
 template <typename X>
@@ -68,7 +54,7 @@ __device__ __forceinline__ void make_table(const RopeArgs& a, unsigned tok, int 
         const int k = i % a.pairs;
         const unsigned at = tok + i / a.pairs, b = at / (unsigned)a.n_tok, t = at % (unsigned)a.n_tok;
         const long long p = a.positions ? a.positions[b * a.pos_stride + t] : a.pos0 + t * a.pos_step;
-        const float2 v = turn((double)p, by_address(&a.f_hi[k]), by_address(&a.f_lo[k]));
+        const float2 v = turn((double)p, by_address(&a.f.hi[k]), by_address(&a.f.lo[k]));
         cs[i] = make_float2(v.x * a.scale, (a.inverse ? -v.y : v.y) * a.scale);
     }
     __syncthreads();
@@ -254,25 +240,15 @@ bool rows_apart(long long d, long long n0, long long s0, long long n1, long long
     return true;
 }
 
-// turns per position of every pair, each as double + float
 void frequencies(const v4a_rope_params& p, RopeArgs* a) {
     const long double two_pi = 6.283185307179586476925286766559005768L;
-    const long double step = powl((long double)p.base, -2.0L / p.rope_dims);
-    long double f = 1.0L;  // radians
-    for (int k = 0; k < a->pairs; ++k, f *= step) {
-        long double g = f;
-        if (p.orig_ctx > 0) {
-            const long double r = (long double)p.orig_ctx * f / two_pi;
-            long double w = (r - (long double)p.beta_slow) / ((long double)p.beta_fast - (long double)p.beta_slow);
-            w = w < 0 ? 0 : w > 1 ? 1 : w;
-            g = f * w + f / (long double)p.factor * (1 - w);
-        } else {
-            g = f / (long double)p.factor;
-        }
-        g /= two_pi;
-        a->f_hi[k] = (double)g;
-        a->f_lo[k] = (float)(g - (long double)a->f_hi[k]);
-    }
+    make_turns(p.rope_dims, p.base, &a->f, [&](long double f) {
+        if (p.orig_ctx == 0) return f / (long double)p.factor;
+        const long double r = (long double)p.orig_ctx * f / two_pi;
+        long double w = (r - (long double)p.beta_slow) / ((long double)p.beta_fast - (long double)p.beta_slow);
+        w = w < 0 ? 0 : w > 1 ? 1 : w;
+        return f * w + f / (long double)p.factor * (1 - w);
+    });
 }
 
 }  // namespace

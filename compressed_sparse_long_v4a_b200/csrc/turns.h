@@ -1,0 +1,42 @@
+// turns.h -- angles of rotary positions: sines and cosines that stay exact to fp32 for positions up to 2^40.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace v4a {
+
+constexpr int kMaxPairs = 256;
+
+// turns (not radians) per position of every pair, each as a sum of two
+struct Turns {
+    double hi[kMaxPairs];
+    float lo[kMaxPairs];
+};
+
+// cos and sin of p f, f = hi + lo turns per position: the product as an exact sum of two doubles, so
+// the fraction of a turn keeps more than 24 bits for |p| up to 2^40
+__device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
+    const double hi = p * f_hi;
+    const double lo = fma(p, f_hi, -hi) + p * (double)f_lo;
+    const double frac = (hi - rint(hi)) + lo;
+    float s, c;
+    sincospif((float)(2.0 * frac), &s, &c);
+    return make_float2(c, s);
+}
+
+// base^(-2k/R) radians per position, k < R / 2, passed through `scale` (radians to radians)
+template <typename F>
+inline void make_turns(int rope_dims, double base, Turns* t, F scale) {
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    const long double step = powl((long double)base, -2.0L / rope_dims);
+    long double f = 1.0L;
+    for (int k = 0; k < rope_dims / 2; ++k, f *= step) {
+        const long double g = scale(f) / two_pi;
+        t->hi[k] = (double)g;
+        t->lo[k] = (float)(g - (long double)t->hi[k]);
+    }
+}
+
+}  // namespace v4a
