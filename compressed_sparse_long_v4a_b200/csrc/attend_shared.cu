@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
+#include "turns.h"
 
 #include <type_traits>
 
@@ -190,62 +191,84 @@ __global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, Si
     }
 }
 
-// one block per row (query, head): joins its pieces
-__global__ void __launch_bounds__(128) shared_join_kernel(SharedArgs a, SimtPlan p, const float2* part_ml, const float* part_o) {
+// One block per row (query, head) joins its pieces: their maxima and sums a thread each, then a warp takes every
+// fourth piece, a lane four neighbouring dims of each 128, with several pieces in flight.
+constexpr int kMaxPieces = 2 * 1024;
+
+__device__ __forceinline__ float block_reduce(float x, float* red, bool max) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = !max ? x + y : isnan(x) || isnan(y) ? NAN : fmaxf(x, y);
+    }
+    __syncthreads();
+    if (lane == 0) red[warp] = x;
+    __syncthreads();
+    x = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) x = !max ? x + red[w] : isnan(x) || isnan(red[w]) ? NAN : fmaxf(x, red[w]);
+    return x;
+}
+
+__global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SimtPlan p,
+                                                               const __grid_constant__ Turns turns, const float2* part_ml, const float* part_o) {
     griddep_wait();
     griddep_launch_dependents();
+    __shared__ float w[kMaxPieces];  // weight of every piece
+    __shared__ __align__(16) float sum[kThreads / 32][512];
+    __shared__ float red[kThreads / 32];
     const long long row = blockIdx.x;
-    const int d = a.d;
+    const int d = a.d, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long query = row / a.heads;
     const int h = (int)(row % a.heads), b = (int)(query / a.n_q);
     const long long t = seq_len(a, b) - a.n_q + query % a.n_q;
     const bool live = has_candidates(a, t);
-    const int n_pre = p.groups ? p.splits : 0, n = n_pre + p.own_splits;
+    const int n_pre = p.groups ? p.splits : 0, n = live ? n_pre + p.own_splits : 0;
     // row of piece i in part_ml / part_o
-    auto piece_row = [&](int i) -> long long {
-        if (i < n_pre) return ((row / kRowsB) * p.splits + i) * kRowsB + row % kRowsB;
-        const long long own = (long long)p.groups * p.splits + (query * p.head_tiles + h / kRowsB) * p.own_splits + (i - n_pre);
-        return own * kRowsB + h % kRowsB;
-    };
+    const long long row_pre = (row / kRowsB) * p.splits * kRowsB + row % kRowsB;
+    const long long row_own = ((long long)p.groups * p.splits + (query * p.head_tiles + h / kRowsB) * p.own_splits) * kRowsB + h % kRowsB;
+    auto piece_row = [&](int i) -> long long { return i < n_pre ? row_pre + (long long)i * kRowsB : row_own + (long long)(i - n_pre) * kRowsB; };
     if (threadIdx.x == 0 && h == 0 && query % a.n_q == 0) report_sequence(a, b);
-    float mmax = -INFINITY;
-    if (live)
-        for (int i = 0; i < n; ++i) {
-            const float m = part_ml[piece_row(i)].x;
-            mmax = isnan(m) || isnan(mmax) ? NAN : fmaxf(mmax, m);
-        }
-    float l = 0.f;
-    if (mmax != -INFINITY) {
-        for (int i = 0; i < n; ++i) {
-            const float2 ml = part_ml[piece_row(i)];
-            if (ml.x != -INFINITY) l += exp2f(ml.x - mmax) * ml.y;
-        }
-        if (a.sink) l += exp2f(a.sink[h] * kLog2eF - mmax);
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float x = part_ml[piece_row(i)].x;
+        m = isnan(x) || isnan(m) ? NAN : fmaxf(m, x);
     }
+    m = block_reduce(m, red, true);
+    float l = 0.f;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float2 ml = part_ml[piece_row(i)];
+        w[i] = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);  // of an empty piece: 0
+        if (ml.x != -INFINITY) l += w[i] * ml.y;
+    }
+    l = block_reduce(l, red, false);  // behind its barriers every weight is written
+    if (a.sink && m != -INFINITY) l += exp2f(a.sink[h] * kLog2eF - m);
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
-    if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (mmax + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
-    const int r0 = d - a.rope_dims;
-    for (int e = threadIdx.x * 2; e < d; e += 256) {
-        float x = 0.f, y = 0.f;
-        if (mmax != -INFINITY) {
-            for (int i = 0; i < n; ++i) {
-                const long long pr = piece_row(i);
-                const float ms = part_ml[pr].x;
-                if (ms == -INFINITY) continue;  // its output was never accumulated
-                const float w = exp2f(ms - mmax);
-                const float2 v = *reinterpret_cast<const float2*>(part_o + pr * d + e);
-                x = fmaf(w, v.x, x);
-                y = fmaf(w, v.y, y);
-            }
+    if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
+    for (int e = lane * 4; e < d; e += 128) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = warp; i < n; i += kThreads / 32) {
+            const float wi = w[i];
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + piece_row(i) * d + e));
+            o.x = fmaf(wi, v.x, o.x);
+            o.y = fmaf(wi, v.y, o.y);
+            o.z = fmaf(wi, v.z, o.z);
+            o.w = fmaf(wi, v.w, o.w);
         }
-        x *= inv;
-        y *= inv;
+        *reinterpret_cast<float4*>(&sum[warp][e]) = o;
+    }
+    __syncthreads();
+    const int r0 = d - a.rope_dims;
+    for (int e = threadIdx.x * 2; e < d; e += 2 * kThreads) {
+        float x = ((sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e])) * inv;
+        float y = ((sum[0][e + 1] + sum[1][e + 1]) + (sum[2][e + 1] + sum[3][e + 1])) * inv;
         if (a.rope_dims > 0 && e >= r0 && live) {
-            float s, c;
-            rope_sincos(t, (e - r0) >> 1, a.rope_dims, a.rope_base, &s, &c);
+            const float2 r = turn((double)t, turns.hi[(e - r0) >> 1], turns.lo[(e - r0) >> 1]);
             const float u = x;
-            x = fmaf(u, c, -y * s);
-            y = fmaf(u, s, y * c);
+            x = fmaf(u, r.x, y * r.y);  // back by the position
+            y = fmaf(y, r.x, -u * r.y);
         }
         if (a.out_dtype == V4A_F32) {
             *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * d + e) = make_float2(x, y);
@@ -342,7 +365,11 @@ cudaError_t simt_attend(const SharedArgs& a, void* ws, cudaStream_t st) {
     if (e == cudaSuccess && pieces > 0)
         e = launch_pdl(kernel, dim3((unsigned)pieces), dim3(kThreads), sizeof(Tile<T, D>), st, a, p, ml, po);
     if (e == cudaSuccess)
-        e = launch_pdl(shared_join_kernel, dim3((unsigned)p.rows), dim3(128), 0, st, a, p, (const float2*)ml, (const float*)po);
+    {
+        Turns turns;
+        if (a.rope_dims > 0) make_turns(a.rope_dims, a.rope_base, &turns);
+        e = launch_pdl(shared_join_kernel, dim3((unsigned)p.rows), dim3(kThreads), 0, st, a, p, turns, (const float2*)ml, (const float*)po);
+    }
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -900,7 +900,7 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     Turns turns;
-    if (a.rope_dims > 0) make_turns(a.rope_dims, a.rope_base, &turns, [](long double f) { return f; });
+    if (a.rope_dims > 0) make_turns(a.rope_dims, a.rope_base, &turns);
     cudaError_t e = launch_pdl(shared_tc_join_kernel, dim3((c.rows + 31) / 32, kD / 16), dim3(128), 0, st, c, turns);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }

@@ -1,17 +1,20 @@
 // evict.cu -- eviction from a cache by accumulated attention weight.
 //
 // Of a sequence's n slots the `budget` heaviest stay (the first and last ones always), moved to the front
-// in order.  The rows that stay are read and written once: that copy bounds the call.  Choosing them is
-// a radix select over order-preserving 32-bit keys of the weights, by a block per sequence, or a cluster
-// of up to 8 where a block's threads would have more than 8 keys each (what a cluster adds is a barrier and reads of
-// the other blocks' counts per pass).  The keys are loaded once and stay in shared memory: three histogram passes of 11, 11 and
-// 10 bits, the counts of a cluster's blocks added up through distributed shared memory, then one ordered
-// pass that places the slots by ballots.  evict_rows_kernel then moves the rows, a warp per row, four rows
-// in flight.
+// in order.  The rows that stay are read and written once: that copy bounds the call.  Choosing them is a
+// radix select over order-preserving 32-bit keys of the weights, by a block per sequence, or a cluster of
+// up to 16 where a block's threads would have more than 8 weights each.  Their keys stay in shared memory.
+// Histogram passes of 11, 11 and 10 bits (a cluster's counts are added up through distributed shared memory) narrow the
+// threshold's digits; as soon as at most 256 candidates share them, which one or two passes usually
+// achieve, the candidates are listed and ranked against each other.  That gives the last
+// slot kept, (key, slot), and one ordered pass places what comes before it by ballots.  The loops are rolled: the
+// code runs cold, and fetching unrolled copies costs more than they save.  evict_rows_kernel then moves
+// the rows, a warp per row, four rows in flight.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 #include <cstddef>
 
@@ -35,50 +38,42 @@ struct EvictArgs {
     int own_rows, out_rows, budget, first, recent, first_entry;
 };
 
+constexpr int kList = 256;  // four threads rank each
+
 struct __align__(16) EvictSmem {
     uint32_t hist[3][kBins];  // this block's counts, by pass
-    uint32_t total[2];        // this block's slots above the threshold, and at it
-    uint32_t pick[2];         // chosen digit, how many of it are still wanted
+    uint32_t sums[3][kBins / 2];  // a cluster's counts of this block's share of the bins
+    uint2 list[kList];        // block 0 of the cluster: candidates, (key, slot)
+    uint2 last;               // ... the last slot kept, (key, slot)
+    uint32_t listed;          // ... how many candidates
+    uint32_t total;           // this block's kept slots, or its candidates
+    uint32_t pick[3];         // the threshold's digit, how many of those who have it are wanted, and how many have it
     uint32_t warp[32];
 };
 
-static_assert(offsetof(EvictSmem, hist) % 8 == 0 && offsetof(EvictSmem, total) % 8 == 0, "read in pairs by other blocks");
+static_assert(offsetof(EvictSmem, hist) % 8 == 0 && offsetof(EvictSmem, sums) % 8 == 0 && offsetof(EvictSmem, list) % 8 == 0 && offsetof(EvictSmem, last) % 8 == 0, "read in pairs");
 
-// exclusive prefix sum over the block's threads; *sum: the block's total
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_s, uint32_t* sum) {
+// Exclusive prefix sum of a number per warp (the same in all its lanes) over the block's warps; *sum: the block's total.  One
+// barrier; the next call's writes to warp_s come behind another one.
+__device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t* warp_s, uint32_t* sum) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_s[w] = x;
+    if (lane == 0) warp_s[w] = v;
     __syncthreads();
-    if (w == 0) {
-        uint32_t y = warp_s[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        warp_s[lane] = y;
-    }
-    __syncthreads();
-    const uint32_t before = w ? warp_s[w - 1] : 0u;
-    *sum = warp_s[31];
-    __syncthreads();
-    return before + x - v;
+    const uint32_t x = warp_s[lane];
+    *sum = __reduce_add_sync(0xffffffffu, x);
+    return __reduce_add_sync(0xffffffffu, lane < w ? x : 0u);
 }
 
 // STORED: the keys stay in (dynamic) shared memory, `rounds` per thread; else they are made again in every pass.
-// Slots ascend over blocks, then warps, then a warp's rounds, then lanes.  The loops are rolled: the code runs cold,
-// and fetching unrolled copies took most of the time (8 keys a thread in registers: 17 us instead of 7).
+// Slots ascend over blocks, then warps, then a warp's rounds, then lanes; slots beyond the count have key 0, the lowest,
+// and come behind the real ones that have it (NaN), so they need no exception.
 template <bool STORED>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     __shared__ EvictSmem sm;
     extern __shared__ uint32_t stored[];
+    constexpr uint32_t kAll = 0xffffffffu;
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+    if (threadIdx.x == 0) sm.listed = 0;
     griddep_wait();  // everything before this kernel on the stream has finished
     griddep_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
@@ -88,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         if (csize > 1) cluster.sync();
         else __syncthreads();
     };
+    EvictSmem& lead = csize > 1 ? *cluster.map_shared_rank(&sm, 0) : sm;
     const int b = blockIdx.x / csize;
     unsigned n = (unsigned)a.own_rows;
     if (a.own_count) {
@@ -101,118 +97,200 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     const unsigned width = (unsigned)csize * kThreads;
     const int rounds = (int)((n + width - 1) / width);
     const unsigned base = ((unsigned)crank * kThreads + warp * 32) * rounds + lane;
-    const unsigned first = (unsigned)a.first, free_slots = n > (unsigned)a.first + a.recent ? n - a.first - a.recent : 0;
-    auto make_key = [&](unsigned i) -> uint32_t {
-        if (i - first >= free_slots) return 0xffffffffu;  // always kept
-        const float x = w[i];
-        return isnan(x) ? 0u : float_to_ordered(x);  // -inf: 0x007fffff, +inf: 0xff800000
-    };
+    uint32_t* const mine_stored = stored + threadIdx.x;  // a thread reads what it copied itself
     if (STORED && !all) {
-#pragma unroll 8
+#pragma unroll 1
         for (int j = 0; j < rounds; ++j)
-            if (base + 32 * j < n) stored[j * kThreads + threadIdx.x] = make_key(base + 32 * j);
+            if (base + 32 * j < n) tc::cp_async_4(mine_stored + j * kThreads, w + base + 32 * j);
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
     }
-    auto key = [&](int j) -> uint32_t { return STORED ? stored[j * kThreads + threadIdx.x] : make_key(base + 32 * j); };
-    // radix select of the want-th largest key; digits of 11, 11 and 10 bits
-    uint32_t prefix = 0, need = want;
+    const unsigned first = (unsigned)a.first, free_slots = n > (unsigned)a.first + a.recent ? n - a.first - a.recent : 0;
+    auto make_key = [&](unsigned i, float x) -> uint32_t {
+        uint32_t k = isnan(x) ? 0u : float_to_ordered(x);  // -inf: 0x007fffff, +inf: 0xff800000
+        if (i - first >= free_slots) k = 0xffffffffu;      // always kept
+        return i < n ? k : 0u;
+    };
+    auto key = [&](int j) -> uint32_t {
+        if (STORED) return mine_stored[j * kThreads];
+        const unsigned i = base + 32 * j;
+        return make_key(i, i < n ? w[i] : 0.f);
+    };
+    // the last slot kept: larger keys and, among equal ones, lower slots come before it
+    uint32_t last_key = 0u, last_slot = 0xffffffffu;
     if (!all) {
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t digits = pass == 2 ? 1024u : 2048u;
-            const uint32_t above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
+        uint32_t prefix = 0, need = want, found = 0;
+        int shift = 32, pass = 0;
+        do {
+            const int bits = pass == 2 ? 10 : 11;
+            const uint32_t digits = 1u << bits;
+            const int above = shift;  // digits already known
+            shift -= bits;
             uint32_t* hist = sm.hist[pass];
-            if (pass == 0) __syncthreads();  // the counts are zero
-#pragma unroll 1
-            for (int j = 0; j < rounds; ++j) {
-                const bool in = base + 32 * j < n;
-                const uint32_t k = in ? key(j) : 0u;
-                const bool mine = in && ((k ^ prefix) & above) == 0;
-                const uint32_t m = __ballot_sync(0xffffffffu, mine);
-                if (m == 0) continue;
-                // equal weights are common, and 32 additions to one counter slow
-                const uint32_t d = (k >> shift) & (digits - 1), d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
-                if (__all_sync(0xffffffffu, !mine || d == d0)) {
-                    if (lane == 0) atomicAdd(&hist[d0], (uint32_t)__popc(m));
-                } else if (mine) {
-                    atomicAdd(&hist[d], 1u);
+            if (pass == 0) {
+                __syncthreads();  // the counts are zero
+#pragma unroll 2
+                for (int j = 0; j < rounds; ++j) {
+                    uint32_t k;
+                    if (STORED) {
+                        const unsigned i = base + 32 * j;
+                        k = make_key(i, __uint_as_float(mine_stored[j * kThreads]));
+                        mine_stored[j * kThreads] = k;
+                    } else {
+                        k = key(j);
+                    }
+                    // equal weights are common, and 32 additions to one counter slow
+                    const uint32_t d = k >> 21;
+                    if (__all_sync(kAll, d == __shfl_sync(kAll, d, 0))) {
+                        if (lane == 0) atomicAdd(&hist[d], 32u);
+                    } else {
+                        atomicAdd(&hist[d], 1u);
+                    }
                 }
-            }
-            sync_all();
-            // this thread's two bins, the highest digits first
-            uint32_t c[2] = {0, 0};
-            const uint32_t d0 = digits - 1 - 2 * threadIdx.x;
-            if (2 * threadIdx.x < digits) {
-                if (csize == 1) {
-                    c[0] = hist[d0];
-                    c[1] = hist[d0 - 1];
-                } else {
-#pragma unroll 4
-                    for (int r = 0; r < csize; ++r) {
-                        const uint2 h = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, r) + d0 - 1);
-                        c[0] += h.y;
-                        c[1] += h.x;
+            } else {
+#pragma unroll 2
+                for (int j = 0; j < rounds; ++j) {
+                    const uint32_t k = key(j);
+                    const bool mine = (k >> above) == (prefix >> above);
+                    const uint32_t m = __ballot_sync(kAll, mine);
+                    if (m == 0) continue;
+                    const uint32_t d = (k >> shift) & (digits - 1), d0 = __shfl_sync(kAll, d, __ffs(m) - 1);
+                    if (__all_sync(kAll, !mine || d == d0)) {
+                        if (lane == 0) atomicAdd(&hist[d0], (uint32_t)__popc(m));
+                    } else if (mine) {
+                        atomicAdd(&hist[d], 1u);
                     }
                 }
             }
-            uint32_t sum;
-            const uint32_t before = block_scan(c[0] + c[1], sm.warp, &sum);
-            if (before < need && need <= before + c[0] + c[1]) {
-                const bool second = need > before + c[0];
+            sync_all();
+            // Two bins per thread, the highest digits first.  In a cluster every block adds up its share of the bins first, so that
+            // each count crosses once.
+            uint32_t c0 = 0, c1 = 0;
+            const uint32_t d0 = digits - 1 - 2 * threadIdx.x;
+            if (csize > 1) {
+                const uint32_t share = digits / csize;
+                if (threadIdx.x < share) {
+                    uint32_t c = 0;
+#pragma unroll 16
+                    for (int r = 0; r < csize; ++r) c += cluster.map_shared_rank(hist, r)[crank * share + threadIdx.x];
+                    sm.sums[pass][threadIdx.x] = c;
+                }
+                cluster.sync();
+                if (2 * threadIdx.x < digits) {
+                    const uint32_t* from = cluster.map_shared_rank(&sm.sums[pass][0], (int)(d0 / share));
+                    const uint2 h = *reinterpret_cast<const uint2*>(from + (d0 - 1) % share);
+                    c0 = h.y;
+                    c1 = h.x;
+                }
+            } else if (2 * threadIdx.x < digits) {
+                const uint2 h = *reinterpret_cast<const uint2*>(hist + d0 - 1);
+                c0 = h.y;
+                c1 = h.x;
+            }
+            uint32_t run = c0 + c1, sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kAll, run, o);
+                if (lane >= o) run += y;
+            }
+            const uint32_t before = warps_before(__shfl_sync(kAll, run, 31), sm.warp, &sum) + run - c0 - c1;
+            if (before < need && need <= before + c0 + c1) {
+                const bool second = need > before + c0;
                 sm.pick[0] = second ? d0 - 1 : d0;
-                sm.pick[1] = need - before - (second ? c[0] : 0u);
+                sm.pick[1] = need - before - (second ? c0 : 0u);
+                sm.pick[2] = second ? c1 : c0;
             }
             __syncthreads();
             prefix |= sm.pick[0] << shift;
             need = sm.pick[1];
-        }
-    }
-    // Slots above the threshold stay, and the first `need` of those at it; with all of them, every slot counts as above.
-    uint32_t gt = 0, eq = 0;
+            found = sm.pick[2];
+            ++pass;
+        } while (found > kList && need < found && shift > 0);
+        auto candidate = [&](int j) { return (key(j) >> shift) == (prefix >> shift); };
+        if (need == found) {  // all of them stay
+            last_key = prefix;
+        } else if (found <= kList) {
 #pragma unroll 1
-    for (int j = 0; j < rounds; ++j) {
-        if (base + 32 * j >= n) continue;
-        const uint32_t k = all ? 0u : key(j);
-        gt += all || k > prefix;
-        eq += !all && k == prefix;
+            for (int j = 0; j < rounds; ++j) {
+                const bool mine = candidate(j);
+                const uint32_t m = __ballot_sync(kAll, mine);
+                if (m == 0) continue;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&lead.listed, (uint32_t)__popc(m));
+                at = __shfl_sync(kAll, at, 0) + __popc(m & ((1u << lane) - 1u));
+                if (mine) lead.list[at] = make_uint2(key(j), base + 32 * j);
+            }
+            sync_all();
+            if (crank == 0) {
+                const uint32_t at = threadIdx.x >> 2;
+                const uint2 me = sm.list[at < found ? at : 0];
+                uint32_t rank = 0;
+#pragma unroll 4
+                for (uint32_t i = threadIdx.x & 3; i < found; i += 4) {
+                    const uint2 o = sm.list[i];
+                    rank += o.x > me.x || (o.x == me.x && o.y < me.y);
+                }
+                rank += __shfl_xor_sync(kAll, rank, 1);
+                rank += __shfl_xor_sync(kAll, rank, 2);
+                if (at < found && rank == need - 1) sm.last = me;
+            }
+            sync_all();
+            last_key = lead.last.x;
+            last_slot = lead.last.y;
+        } else {  // more equal keys than the list holds: the need-th of them in the order of the slots
+            uint32_t mine = 0, sum;
+#pragma unroll 1
+            for (int j = 0; j < rounds; ++j) mine += candidate(j);
+            mine = __reduce_add_sync(kAll, mine);
+            uint32_t at = warps_before(mine, sm.warp, &sum);
+            if (threadIdx.x == 0) sm.total = sum;
+            sync_all();
+            for (int r = 0; r < crank; ++r) at += *cluster.map_shared_rank(&sm.total, r);
+            if (at < need && need <= at + mine) {
+#pragma unroll 1
+                for (int j = 0; j < rounds; ++j) {
+                    const uint32_t m = __ballot_sync(kAll, candidate(j));
+                    if (((m >> lane) & 1) && at + __popc(m & ((1u << lane) - 1u)) == need - 1) lead.last = make_uint2(prefix, base + 32 * j);
+                    at += __popc(m);
+                }
+            }
+            sync_all();
+            last_key = prefix;
+            last_slot = lead.last.y;
+        }
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);  // of this warp
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    uint32_t sum_gt, sum_eq;
-    uint32_t at_gt = block_scan(lane == 0 ? gt : 0u, sm.warp, &sum_gt), at_eq = block_scan(lane == 0 ? eq : 0u, sm.warp, &sum_eq);
-    at_gt = __shfl_sync(0xffffffffu, at_gt, 0);
-    at_eq = __shfl_sync(0xffffffffu, at_eq, 0);
+    auto stays = [&](int j) {
+        const unsigned i = base + 32 * j;
+        if (all) return i < n;
+        const uint32_t k = key(j);
+        return k > last_key || (k == last_key && i <= last_slot);
+    };
+    uint32_t mine = 0, sum;
+#pragma unroll 2
+    for (int j = 0; j < rounds; ++j) mine += stays(j);
+    __syncthreads();  // sm.warp was read
+    uint32_t at = warps_before(__reduce_add_sync(kAll, mine), sm.warp, &sum);
     if (csize > 1) {
-        if (threadIdx.x == 0) {
-            sm.total[0] = sum_gt;
-            sm.total[1] = sum_eq;
-        }
+        cluster.sync();  // sm.total was read
+        if (threadIdx.x == 0) sm.total = sum;
         cluster.sync();
-        for (int r = 0; r < crank; ++r) {
-            const uint2 t = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sm.total, r));
-            at_gt += t.x;
-            at_eq += t.y;
-        }
+        for (int r = 0; r < crank; ++r) at += *cluster.map_shared_rank(&sm.total, r);
     }
     int32_t* kept = a.kept + (long long)b * a.budget;
     const long long orow = (long long)b * a.out_rows;
-    const uint32_t below = (1u << lane) - 1u;
+    float* weights_out = a.weights_out + orow;
+    int32_t* entry_out = a.entry_out ? a.entry_out + orow : nullptr;
+    const int32_t* own_entry = a.own_entry ? a.own_entry + (long long)b * a.own_rows : nullptr;
 #pragma unroll 2
     for (int j = 0; j < rounds; ++j) {
-        const unsigned i = base + 32 * j;
-        const bool in = i < n;
-        const uint32_t k = in && !all ? key(j) : 0u;
-        const bool is_gt = in && (all || k > prefix), is_eq = in && !all && k == prefix;
-        const uint32_t m_gt = __ballot_sync(0xffffffffu, is_gt), m_eq = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t g = at_gt + __popc(m_gt & below), r = at_eq + __popc(m_eq & below);
-        at_gt += __popc(m_gt);
-        at_eq += __popc(m_eq);
-        if (is_gt || (is_eq && r < need)) {
-            const uint32_t pos = g + (r < need ? r : need);  // the slots kept before this one
+        const bool s = stays(j);
+        const uint32_t m = __ballot_sync(kAll, s), pos = at + __popc(m & ((1u << lane) - 1u));
+        at += __popc(m);
+        if (s) {
+            const unsigned i = base + 32 * j;
             kept[pos] = (int32_t)i;
-            a.weights_out[orow + pos] = w[i];
-            if (a.entry_out)
-                a.entry_out[orow + pos] = a.own_entry ? a.own_entry[(long long)b * a.own_rows + i] : a.first_entry + (int)i;
+            weights_out[pos] = w[i];
+            if (entry_out) entry_out[pos] = own_entry ? own_entry[i] : a.first_entry + (int)i;
         }
     }
     // pad the list
@@ -225,7 +303,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
 __global__ void __launch_bounds__(256) evict_rows_kernel(const uint4* own, uint4* own_out, const int32_t* kept,
                                                          int own_rows, int out_rows, int budget, int chunks) {
     griddep_wait();
-    griddep_launch_dependents();
+    // no early griddep_launch_dependents: blocks of the next kernel that wait here take room from the copies in flight
+    // (32 caches of 8,192 rows: 41 us without, 51 with)
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     const long long p0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
     if (p0 >= budget) return;
@@ -308,15 +387,40 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     a.first = keep_first;
     a.recent = keep_recent;
     a.first_entry = io->first_entry;
-    // a cluster of up to 8 blocks (the portable size) per sequence: as many as leave each thread at most 8 keys
+    // a cluster per sequence, as many blocks as leave each thread at most 8 weights: up to 8, which every device
+    // schedules, or 16 where this one does
     int cs = 1;
-    while (cs < 8 && (long long)cs * kThreads * 8 < io->own_rows) cs *= 2;
-    const long long per = ((long long)io->own_rows + cs * kThreads - 1) / (cs * kThreads);
-    const bool keep = per <= 48;  // 4 KB each
-    auto* kernel = keep ? evict_select_kernel<true> : evict_select_kernel<false>;
-    const size_t smem = keep ? (size_t)per * kThreads * 4 : 0;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = launch_pdl_cluster(kernel, dim3((unsigned)(batch * cs)), dim3(kThreads), smem, st, cs, a);
+    while (cs < 16 && (long long)cs * kThreads * 8 < io->own_rows) cs *= 2;
+    cudaError_t e = cudaSuccess;
+    auto launch = [&](int blocks) {
+        const long long per = ((long long)io->own_rows + blocks * kThreads - 1) / (blocks * kThreads);
+        const bool keep = per <= 44;  // 4 KB each
+        auto* kernel = keep ? evict_select_kernel<true> : evict_select_kernel<false>;
+        const size_t smem = keep ? (size_t)per * kThreads * 4 : 0;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess && blocks > 8) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)blocks);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)blocks;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int fit = 0;
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+            if (e != cudaSuccess || fit < 1) {
+                cudaGetLastError();
+                return false;
+            }
+        }
+        if (e == cudaSuccess) e = launch_pdl_cluster(kernel, dim3((unsigned)(batch * blocks)), dim3(kThreads), smem, st, blocks, a);
+        return true;
+    };
+    if (!launch(cs)) launch(8);
     if (e == cudaSuccess && io->own_rows > 0)
         e = launch_pdl(evict_rows_kernel, dim3((unsigned)((budget + 31) / 32), (unsigned)batch), dim3(256), 0, st,
                        static_cast<const uint4*>(io->own), static_cast<uint4*>(io->own_out), (const int32_t*)io->kept,

@@ -240,17 +240,6 @@ bool rows_apart(long long d, long long n0, long long s0, long long n1, long long
     return true;
 }
 
-void frequencies(const v4a_rope_params& p, RopeArgs* a) {
-    const long double two_pi = 6.283185307179586476925286766559005768L;
-    make_turns(p.rope_dims, p.base, &a->f, [&](long double f) {
-        if (p.orig_ctx == 0) return f / (long double)p.factor;
-        const long double r = (long double)p.orig_ctx * f / two_pi;
-        long double w = (r - (long double)p.beta_slow) / ((long double)p.beta_fast - (long double)p.beta_slow);
-        w = w < 0 ? 0 : w > 1 ? 1 : w;
-        return f * w + f / (long double)p.factor * (1 - w);
-    });
-}
-
 }  // namespace
 }  // namespace v4a
 
@@ -327,7 +316,7 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
     a.pos_stride = pos_stride;
     a.pos0 = pos0;
     a.pos_step = pos_step;
-    frequencies(p, &a);
+    make_turns(p.rope_dims, p.base, &a.f, p.factor, p.orig_ctx, p.beta_fast, p.beta_slow);
     const long long tokens = (long long)batch * n_tok;
     a.all_tok = (unsigned)tokens;
     const long long want = (8LL * kNumSMs + tokens - 1) / tokens;  // blocks per token that fill the SMs

@@ -26,14 +26,22 @@ __device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
     return make_float2(c, s);
 }
 
-// base^(-2k/R) radians per position, k < R / 2, passed through `scale` (radians to radians)
-template <typename F>
-inline void make_turns(int rope_dims, double base, Turns* t, F scale) {
+// base^(-2k/R) radians per position, k < R / 2, extended by `factor` (1: not): divided by it, or, with an original
+// length orig_ctx, those pairs only that turn less than beta_slow times over it, blended up to beta_fast
+inline void make_turns(int rope_dims, double base, Turns* t, double factor = 1, long long orig_ctx = 0, double beta_fast = 0,
+                       double beta_slow = 0) {
     const long double two_pi = 6.283185307179586476925286766559005768L;
     const long double step = powl((long double)base, -2.0L / rope_dims);
     long double f = 1.0L;
     for (int k = 0; k < rope_dims / 2; ++k, f *= step) {
-        const long double g = scale(f) / two_pi;
+        long double g = f / (long double)factor;
+        if (orig_ctx > 0) {
+            const long double r = (long double)orig_ctx * f / two_pi;
+            long double w = (r - (long double)beta_slow) / ((long double)beta_fast - (long double)beta_slow);
+            w = w < 0 ? 0 : w > 1 ? 1 : w;
+            g = f * w + g * (1 - w);
+        }
+        g /= two_pi;
         t->hi[k] = (double)g;
         t->lo[k] = (float)(g - (long double)t->hi[k]);
     }
