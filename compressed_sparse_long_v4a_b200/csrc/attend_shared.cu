@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
+#include "tc.cuh"
 #include "turns.h"
 
 #include <type_traits>
@@ -40,20 +41,42 @@ struct SimtPlan {
 };
 
 template <typename T, int D>
-struct Tile {
+struct __align__(16) Tile {
     float k[kKeys][D + 4];
     float q[kRowsB][D];
-    int ok[kKeys];
+    const T* src[kKeys];  // null: a key that no row sees
 };
 
-// stage one row of d elements (null: zeros) as fp32, by the lanes of one warp
-template <typename T, int D>
-__device__ __forceinline__ void stage_row(float* dst, const T* src, int lane) {
-    for (int c = lane * 8; c < D; c += 256) {
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (src) Vec8<T>::load_nc(src + c, f);
-        *reinterpret_cast<float4*>(dst + c) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(dst + c + 4) = make_float4(f[4], f[5], f[6], f[7]);
+// Rows of D elements as fp32 in shared memory, by a block of N threads: row i from src(i) (null: zeros).  The copies of
+// all rows are in flight together (fp32: asynchronous; the caller waits for them).
+template <typename T, int D, int N, int STRIDE, typename F>
+__device__ __forceinline__ void stage_rows(float (*dst)[STRIDE], int rows, const T* any, F src) {
+    if constexpr (sizeof(T) == 4) {
+        constexpr int kC = D / 4;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < rows * kC; i += N) {
+            const int r = i / kC, c = i % kC * 4;
+            const T* p = src(r);
+            tc::cp_async_16_or_zero(&dst[r][c], p ? p + c : any, p != nullptr);
+        }
+    } else {
+        constexpr int kC = D / 8, kU = 4;
+        for (int i0 = threadIdx.x; i0 < rows * kC; i0 += kU * N) {
+            float f[kU][8];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int i = i0 + u * N;
+                const T* p = i < rows * kC ? src(i / kC) : nullptr;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
+                if (p) Vec8<T>::load_nc(p + i % kC * 8, f[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int i = i0 + u * N;
+                if (i < rows * kC) Vec8<float>::store(&dst[i / kC][i % kC * 8], f[u]);
+            }
+        }
     }
 }
 
@@ -115,8 +138,8 @@ __global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, Si
         k1 = k0 + per < p.own_keys ? k0 + per : p.own_keys;
         if (!has_candidates(a, t)) k1 = k0;
     }
-    for (int r = warp; r < kRowsB; r += kThreads / 32)
-        stage_row<T, D>(sm.q[r], r < n_rows ? static_cast<const T*>(a.q) + (row0 + r) * D : nullptr, lane);
+    const T* const q = static_cast<const T*>(a.q);
+    stage_rows<T, D, kThreads>(sm.q, kRowsB, q, [&](int r) { return r < n_rows ? q + (row0 + r) * D : nullptr; });
     constexpr int kE = D / 32;  // output elements per lane and row, in groups of 4 (2 for D = 64)
     constexpr int kV = kE < 4 ? kE : 4;
     float o[kRw][kE], m_run[kRw], l_run[kRw];
@@ -130,8 +153,8 @@ __global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, Si
     const float scale = kLog2eF / sqrtf((float)D);
     for (long long base = k0; base < k1; base += kKeys) {
         __syncthreads();
-        for (int i = warp; i < kKeys; i += kThreads / 32) {
-            const long long c = base + i;
+        if (threadIdx.x < kKeys) {
+            const long long c = base + threadIdx.x;
             const T* src = nullptr;
             if (c < k1) {
                 if (pre) {
@@ -143,13 +166,16 @@ __global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, Si
                     if (pos >= 0) src = static_cast<const T*>(a.ring) + ((long long)b * a.ring_rows + pos % a.ring_rows) * D;
                 }
             }
-            stage_row<T, D>(sm.k[i], src, lane);
-            if (lane == 0) sm.ok[i] = src != nullptr;
+            sm.src[threadIdx.x] = src;
         }
+        __syncthreads();
+        stage_rows<T, D, kThreads>(sm.k, kKeys, q, [&](int r) { return sm.src[r]; });
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
         __syncthreads();
         float s[kRw];
         dots<D>(sm.k[lane], &sm.q[warp * kRw], s);
-        const bool ok = sm.ok[lane];
+        const bool ok = sm.src[lane] != nullptr;
 #pragma unroll
         for (int r = 0; r < kRw; ++r) {
             const float x = ok ? s[r] * scale : -INFINITY;
@@ -178,6 +204,8 @@ __global__ void __launch_bounds__(kThreads) shared_split_kernel(SharedArgs a, Si
                 for (int e = 0; e < kE; ++e) o[r][e] = fmaf(pj[r], v[e], o[r][e]);
         }
     }
+    tc::cp_async_commit();  // of a piece without keys
+    tc::cp_async_wait<0>();
 #pragma unroll
     for (int r = 0; r < kRw; ++r) {
         const float l = group_sum<32>(l_run[r]);
@@ -278,51 +306,72 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_cons
     }
 }
 
-// Weights: a block takes 32 own slots of one sequence and runs over the sequence's rows (query, head), 16 at
-// a time.  A warp's lane is a slot; the four warps' sums are added in a fixed order.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) weights_kernel(SharedArgs a) {
+// Weights, fp32: a block takes 32 own slots of one sequence and runs over the sequence's rows (query, head), 32 at
+// a time.  A warp's lane is a slot; the eight warps' sums are added in a fixed order.
+constexpr int kWThreads = 256;
+constexpr int kWRows = kWThreads / 32 * kRw;
+
+template <int D>
+struct __align__(16) WeightTile {
+    float k[kKeys][D + 4];
+    float q[kWRows][D];
+    float lse[kWRows];      // times log2 e; -inf: no candidates, or no such row
+    long long seen[kWRows];
+    float sums[kWThreads / 32][kKeys];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWThreads) weights_kernel(SharedArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Tile<T, D>& sm = *reinterpret_cast<Tile<T, D>*>(smem_raw);
-    __shared__ float sums[kThreads / 32][kKeys];
+    WeightTile<D>& sm = *reinterpret_cast<WeightTile<D>*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y, i0 = blockIdx.x * kKeys, count = own_slots(a, b);
     if (blockIdx.x == 0 && threadIdx.x == 0) report_sequence(a, b);
     if (i0 >= count) return;
-    const long long len = seq_len(a, b);
-    for (int i = warp; i < kKeys; i += kThreads / 32)
-        stage_row<T, D>(sm.k[i], i0 + i < count ? static_cast<const T*>(a.own) + ((long long)b * a.own_rows + i0 + i) * D : nullptr, lane);
-    const int slot = i0 + lane;
-    long long e = -1;  // this lane's entry
-    if (slot < count) e = a.own_entry ? (long long)a.own_entry[(long long)b * a.own_rows + slot] : a.n_prefix + slot;
-    const float scale = kLog2eF / sqrtf((float)D);
+    const float* const q = static_cast<const float*>(a.q);
+    const float* const own = static_cast<const float*>(a.own) + ((long long)b * a.own_rows + i0) * D;
     const int n = a.n_q * a.heads;
     const long long row0 = (long long)b * n;
+    stage_rows<float, D, kWThreads>(sm.k, kKeys, q, [&](int r) { return i0 + r < count ? own + (long long)r * D : nullptr; });
+    const int slot = i0 + lane;
+    const long long at = (long long)b * a.own_rows + slot;
+    long long e = -1;  // this lane's entry
+    float before = 0.f;
+    if (slot < count) {
+        e = a.own_entry ? (long long)a.own_entry[at] : a.n_prefix + slot;
+        if (warp == 0 && a.decay != 0.f) before = a.weights_in[at];
+    }
+    const long long len = seq_len(a, b);
+    const float scale = kLog2eF / sqrtf((float)D);
     float got = 0.f;
-    for (int base = 0; base < n; base += kRowsB) {
+    for (int base = 0; base < n; base += kWRows) {
         __syncthreads();
-        for (int r = warp; r < kRowsB; r += kThreads / 32)
-            stage_row<T, D>(sm.q[r], base + r < n ? static_cast<const T*>(a.q) + (row0 + base + r) * D : nullptr, lane);
+        stage_rows<float, D, kWThreads>(sm.q, kWRows, q, [&](int r) { return base + r < n ? q + (row0 + base + r) * D : nullptr; });
+        if (threadIdx.x < kWRows) {
+            const int i = base + threadIdx.x;
+            sm.lse[threadIdx.x] = i < n ? a.lse[row0 + i] * kLog2eF : -INFINITY;
+            sm.seen[threadIdx.x] = i < n ? seen_entries(a, len - a.n_q + i / a.heads) : 0;
+        }
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
         __syncthreads();
         float s[kRw];
         dots<D>(sm.k[lane], &sm.q[warp * kRw], s);
 #pragma unroll
         for (int r = 0; r < kRw; ++r) {
-            const int i = base + warp * kRw + r;
-            if (i >= n) continue;
-            const float lse = a.lse[row0 + i];
-            const long long seen = seen_entries(a, len - a.n_q + i / a.heads);
-            if (e >= 0 && e < seen && lse != -INFINITY) got += exp2f(fmaf(s[r], scale, -lse * kLog2eF));
+            const float lse = sm.lse[warp * kRw + r];
+            if (e >= 0 && e < sm.seen[warp * kRw + r] && lse != -INFINITY) got += exp2f(fmaf(s[r], scale, -lse));
         }
     }
-    sums[warp][lane] = got;
+    sm.sums[warp][lane] = got;
     __syncthreads();
     if (warp == 0 && slot < count) {
-        const long long at = (long long)b * a.own_rows + slot;
-        const float total = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
-        a.weights_out[at] = a.decay == 0.f ? total : fmaf(a.decay, a.weights_in[at], total);
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWThreads / 32; ++w) total += sm.sums[w][lane];
+        a.weights_out[at] = a.decay == 0.f ? total : fmaf(a.decay, before, total);
     }
 }
 
@@ -373,13 +422,13 @@ cudaError_t simt_attend(const SharedArgs& a, void* ws, cudaStream_t st) {
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t simt_weights(const SharedArgs& a, cudaStream_t st) {
-    auto* kernel = weights_kernel<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Tile<T, D>));
+    auto* kernel = weights_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WeightTile<D>));
     if (e == cudaSuccess)
-        e = launch_pdl(kernel, dim3((unsigned)((a.own_rows + kKeys - 1) / kKeys), (unsigned)a.batch), dim3(kThreads),
-                       sizeof(Tile<T, D>), st, a);
+        e = launch_pdl(kernel, dim3((unsigned)((a.own_rows + kKeys - 1) / kKeys), (unsigned)a.batch), dim3(kWThreads),
+                       sizeof(WeightTile<D>), st, a);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -390,7 +439,7 @@ cudaError_t by_shape(const SharedArgs& a, F f) {
     case 64: return f32 ? f(0.f, std::integral_constant<int, 64>()) : f(__nv_bfloat16(), std::integral_constant<int, 64>());
     case 128: return f32 ? f(0.f, std::integral_constant<int, 128>()) : f(__nv_bfloat16(), std::integral_constant<int, 128>());
     case 256: return f32 ? f(0.f, std::integral_constant<int, 256>()) : f(__nv_bfloat16(), std::integral_constant<int, 256>());
-    default: return f32 ? f(0.f, std::integral_constant<int, 512>()) : f(__nv_bfloat16(), std::integral_constant<int, 512>());
+    default: return f(0.f, std::integral_constant<int, 512>());  // bf16: the tensor-core kernels
     }
 }
 
@@ -411,6 +460,8 @@ v4a_status shared_args(const char* what, const void* q, const v4a_shared_cache* 
         return report(V4A_ERR_INVALID_ARG, "%s: n_prefix must be in 0..ctx_len / m", what);
     if (c->own_rows < 0 || c->own_rows > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: own_rows out of range", what);
     if (s->window < 0 || s->window > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: window must be >= 0", what);
+    if (c->n_prefix + (long long)s->batch * ((long long)c->own_rows + s->window + s->n_q) >= 1LL << 31)
+        return report(V4A_ERR_UNSUPPORTED, "%s: n_prefix + batch * (own_rows + window + n_q) must be < 2^31", what);
     if (s->batch > 0 && (!q || (c->own_rows > 0 && !c->own))) return report(V4A_ERR_INVALID_ARG, "%s: q and own are required", what);
     if (!aligned(q, 16) || !aligned(c->own, 16) || !aligned(c->prefix, 16) || !aligned(c->ring, 16))
         return report(V4A_ERR_INVALID_ARG, "%s: q, prefix, own and ring must be 16-byte aligned", what);
@@ -493,7 +544,8 @@ v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, v
 size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_prefix, int own_rows, v4a_dtype dtype) {
     using namespace v4a;
     if (!shape || shape->batch < 1 || shape->n_q < 1 || shape->heads < 1 || shape->heads > 1024 || shape->d < 64 ||
-        shape->d > 512 || shape->window < 0 || n_prefix < 0 || own_rows < 0 || (long long)shape->batch * shape->n_q > 65535)
+        shape->d > 512 || shape->window < 0 || n_prefix < 0 || own_rows < 0 || (long long)shape->batch * shape->n_q > 65535 ||
+        n_prefix >= 1LL << 31 || n_prefix + (long long)shape->batch * ((long long)own_rows + shape->window + shape->n_q) >= 1LL << 31)
         return 0;
     SharedArgs a = {};
     a.batch = shape->batch;
@@ -531,8 +583,13 @@ v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, cons
         if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
     }
     if (a.own_rows == 0) return V4A_OK;
-    if (weights_tc_shape_ok(a)) return from_cuda(launch_weights_tc(a, s), what);
-    return from_cuda(by_shape(a, [&](auto t, auto d) { return simt_weights<decltype(t), decltype(d)::value>(a, s); }), what);
+    if (a.dtype == V4A_BF16) return from_cuda(launch_weights_tc(a, s), what);
+    switch (a.d) {
+    case 64: return from_cuda(simt_weights<64>(a, s), what);
+    case 128: return from_cuda(simt_weights<128>(a, s), what);
+    case 256: return from_cuda(simt_weights<256>(a, s), what);
+    default: return from_cuda(simt_weights<512>(a, s), what);
+    }
 }
 
 }  // extern "C"

@@ -75,7 +75,7 @@ struct __align__(1024) Smem {
     uint8_t kv[kStages][kXBytes];
     uint8_t p[2][kHalf * 128];  // by half of the keys
     Tile tile[kStages];  // what each stage holds
-    float mx[2][4][kHalf];  // row maxima of a tile's quarters, by tile parity
+    float mx[4][kHalf];  // row maxima of a tile's quarters
     float ls[4][kHalf];
     // x_full, z_ready, p_full and q_full count in CTA 0 only
     uint64_t told[kStages], x_full[kStages][2], z_full[kStages], z_ready[kStages], kv_empty[kStages][2], s_full[kStages];
@@ -515,33 +515,40 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int k = 4; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
-        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));  // of NaN alone: NaN
-        sm.mx[j & 1][quarter][r] = mt;
-        if (tc::named_barrier_or(1, 256, odd || !ok)) {
-            if (tc::named_barrier_or(1, 256, !ok)) {
-                ok = false;
-                break;
-            }
-            odd = true;
-        }
-        mt = fmaxf(fmaxf(sm.mx[j & 1][0][r], sm.mx[j & 1][1][r]), fmaxf(sm.mx[j & 1][2][r], sm.mx[j & 1][3][r])) * c.scale_log2;
-        float alpha = 1.f;
-        if (mt > m_run + kSlack) {
-            if (m_run != -INFINITY) alpha = exp2f(m_run - mt);
-            m_run = mt;
-        }
-        l_run *= alpha;
-        const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
+        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c.scale_log2;  // of NaN alone: NaN
+        // The weights are taken against the maximum so far.  Where that was too low for some row, the four threads of each row agree on
+        // a new one and take them again: at the start of a piece, hardly ever later.
         uint32_t pk[16];
-        float ls[2] = {0.f, 0.f};
+        float ls[2], alpha = 1.f;
+        bool leave = false, settled = false;
+#pragma unroll 1
+        for (;;) {
+            const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
+            ls[0] = ls[1] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
-            ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
-            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+            for (int k = 0; k < 16; ++k) {
+                const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
+                ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
+                const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+                pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+            }
+            if (settled || !tc::named_barrier_or(1, 256, mt > m_run + kSlack || odd || !ok)) break;
+            settled = true;
+            sm.mx[quarter][r] = mt;
+            leave = tc::named_barrier_or(1, 256, !ok);
+            if (leave) break;
+            odd = tc::named_barrier_or(1, 256, odd);
+            mt = fmaxf(fmaxf(sm.mx[0][r], sm.mx[1][r]), fmaxf(sm.mx[2][r], sm.mx[3][r]));
+            if (mt > m_run + kSlack) {
+                if (m_run != -INFINITY) alpha = exp2f(m_run - mt);
+                m_run = mt;
+            }
         }
-        l_run += ls[0] + ls[1];
+        if (leave) {
+            ok = false;
+            break;
+        }
+        l_run = l_run * alpha + (ls[0] + ls[1]);
         // P and O are free once the product of the tile before is done
         const bool free = j == 0 || wait(&sm.p_free, (j - 1) & 1);
         if (__any_sync(kAll, alpha != 1.f) && free) {
@@ -867,8 +874,7 @@ long long pieces(const PairArgs& c) { return c.total > 0 ? (long long)c.groups +
 }  // namespace
 
 bool shared_tc_shape_ok(const SharedArgs& a) {
-    return a.dtype == V4A_BF16 && a.d == kD &&
-           (long long)a.n_prefix + (long long)a.batch * ((long long)a.own_rows + a.window + a.n_q) < (1LL << 31);
+    return a.dtype == V4A_BF16 && a.d == kD;
 }
 
 size_t shared_tc_workspace_bytes(const SharedArgs& a) {

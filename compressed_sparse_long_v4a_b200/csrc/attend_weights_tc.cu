@@ -330,10 +330,6 @@ bool make_map(CUtensorMap* map, const void* base, long long n, long long rows, i
 
 }  // namespace
 
-bool weights_tc_shape_ok(const SharedArgs& a) {
-    return a.dtype == V4A_BF16 && a.n_prefix + (long long)a.own_rows < (1LL << 31);
-}
-
 cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t st) {
     WeightArgs c;
     c.a = a;

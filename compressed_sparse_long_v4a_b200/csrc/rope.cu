@@ -23,8 +23,8 @@ struct RopeStream {
     void* out;
     int heads, off;
     int rot, row_items;  // items of a row: rotated ones first, then the copied ones
-    // vectors: tokens per block (1 unless a token's rows fill less than half of it), heads side by side in it, and the
-    // blocks that a token's heads and columns are cut over; any alignment: blocks per token (h_parts)
+    // vectors: tokens per block (1 unless a token's rows fit into it), heads side by side in it, and the blocks that a
+    // token's heads and columns are cut over; any alignment: blocks per token (h_parts)
     int tokens, h_par, h_parts, c_parts;
     unsigned block0;     // its first block
     long long xb, xt, xh, ob, ot, oh;
@@ -82,6 +82,31 @@ struct Item {
     __device__ __forceinline__ void set(const float (&f)[8]) { Vec8<T>::store(reinterpret_cast<T*>(w), f); }
 };
 
+// the pairs of a rotated item (u, and in the half layout v) turned by w
+template <typename T, bool HALF>
+__device__ __forceinline__ void rotate(Item<T>& u, Item<T>& v, const float2* w) {
+    float x[8], y[8];
+    u.get(x);
+    if (HALF) {
+        v.get(y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float p = x[k], q = y[k];
+            x[k] = p * w[k].x - q * w[k].y;
+            y[k] = q * w[k].x + p * w[k].y;
+        }
+        v.set(y);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float p = x[2 * k], q = x[2 * k + 1];
+            x[2 * k] = p * w[k].x - q * w[k].y;
+            x[2 * k + 1] = q * w[k].x + p * w[k].y;
+        }
+    }
+    u.set(x);
+}
+
 // Rows, offsets and strides in multiples of 8 elements: an item is one 8-element chunk, or, in the half
 // layout, the two chunks that a rotated item pairs up.
 template <typename T, bool HALF>
@@ -89,98 +114,108 @@ __global__ void __launch_bounds__(kThreads, 4) rope_vec_kernel(const __grid_cons
     __shared__ __align__(16) float2 cs[kTable];
     griddep_wait();  // everything before this kernel on the stream has finished
     const RopeStream& s = which_stream(a);
-    const int parts = s.h_parts * s.c_parts;
-    const unsigned local = blockIdx.x - s.block0, group = local / (unsigned)parts;
-    const int part = (int)(local % (unsigned)parts), c_part = part % s.c_parts;
-    const unsigned tok0 = group * (unsigned)s.tokens;
-    const int n_tok = (int)min((unsigned)s.tokens, a.all_tok - tok0);
-    // this thread's column c, token and first head
-    int c, h, i_tok = 0;
-    bool on;
-    if (s.c_parts > 1) {
-        c = c_part * kThreads + threadIdx.x;
-        h = part / s.c_parts;
-        on = c < s.row_items;
-    } else {
-        const int r = (int)threadIdx.x / s.row_items;
-        c = (int)threadIdx.x - r * s.row_items;
-        if (s.tokens > 1) {
-            i_tok = r / s.heads;
-            h = r - i_tok * s.heads;
-            on = i_tok < n_tok;
-        } else {
-            h = part * s.h_par + r;
-            on = r < s.h_par;
-        }
-    }
-    const int step = s.h_par * s.h_parts;  // tokens > 1: all heads at once
-    const unsigned tok = tok0 + i_tok, b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
-    const bool rotated = c < s.rot;
-    int e = 8 * (rotated ? c : c - s.rot);
-    if (rotated) e += s.off;
-    else if (e >= s.off) e += 2 * a.pairs;
-    const T* xp = static_cast<const T*>(s.x) + b * s.xb + t * s.xt + e;
-    T* op = static_cast<T*>(s.out) + b * s.ob + t * s.ot + e;
     constexpr int kU = sizeof(T) == 2 ? 4 : 2;  // rows in flight
     constexpr int kA = HALF ? 8 : 4;            // pairs of an item
-    if (!on) h = s.heads;
+    const int parts = s.h_parts * s.c_parts;
+    const unsigned local = blockIdx.x - s.block0, group = local / (unsigned)parts;
+    const unsigned tok0 = group * (unsigned)s.tokens;
+    const int n_tok = (int)min((unsigned)s.tokens, a.all_tok - tok0);
     Item<T> u[kU], v[kU];
-    auto load = [&]() {
-#pragma unroll
-        for (int j = 0; j < kU; ++j) {
-            const int hj = h + j * step;
-            if (hj >= s.heads) continue;
-            u[j].load(xp + hj * s.xh);
-            if (HALF && rotated) v[j].load(xp + hj * s.xh + a.pairs);
-        }
-    };
-    load();  // on its way while the angles are worked out
-    make_table(a, tok0, n_tok, cs);
     float2 w[kA];
-    if (on && rotated) {
+    auto angles = [&](int at) {
 #pragma unroll
         for (int k = 0; k < kA; k += 2) {
-            const float4 x = *reinterpret_cast<const float4*>(&cs[i_tok * a.pairs + kA * c + k]);
+            const float4 x = *reinterpret_cast<const float4*>(&cs[at + k]);
             w[k] = make_float2(x.x, x.y);
             w[k + 1] = make_float2(x.z, x.w);
         }
-    }
-    while (h < s.heads) {
-        if (rotated) {
+    };
+    auto element = [&](int c) {  // where item c of a row begins
+        const int e = 8 * (c < s.rot ? c : c - s.rot);
+        return c < s.rot ? e + s.off : e >= s.off ? e + 2 * a.pairs : e;
+    };
+    if (s.tokens > 1) {
+        // several tokens, a row of threads for each of their rows
+        const int per_tok = s.heads * s.row_items, items = n_tok * per_tok;
+        const T* xp[kU];
+        T* op[kU];
+        int at[kU];  // angles of a rotated item; -1: copied; -2: none
+        auto load = [&](int i0) {
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                if (h + j * step >= s.heads) continue;
-                float x[8], y[8];
-                u[j].get(x);
-                if (HALF) {
-                    v[j].get(y);
+                const int i = i0 + j * kThreads;
+                at[j] = -2;
+                if (i >= items) continue;
+                const int i_tok = i / per_tok, r = i - i_tok * per_tok, h = r / s.row_items, c = r - h * s.row_items;
+                const unsigned tok = tok0 + i_tok, b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
+                const int e = element(c);
+                at[j] = c < s.rot ? i_tok * a.pairs + kA * c : -1;
+                xp[j] = static_cast<const T*>(s.x) + b * s.xb + t * s.xt + h * s.xh + e;
+                op[j] = static_cast<T*>(s.out) + b * s.ob + t * s.ot + h * s.oh + e;
+                u[j].load(xp[j]);
+                if (HALF && at[j] >= 0) v[j].load(xp[j] + a.pairs);
+            }
+        };
+        load(threadIdx.x);  // on its way while the angles are worked out
+        make_table(a, tok0, n_tok, cs);
+        for (int i0 = threadIdx.x; i0 < items; i0 += kU * kThreads, load(i0)) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float p = x[k], q = y[k];
-                        x[k] = p * w[k % kA].x - q * w[k % kA].y;
-                        y[k] = q * w[k % kA].x + p * w[k % kA].y;
-                    }
-                    v[j].set(y);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float p = x[2 * k], q = x[2 * k + 1];
-                        x[2 * k] = p * w[k].x - q * w[k].y;
-                        x[2 * k + 1] = q * w[k].x + p * w[k].y;
-                    }
+            for (int j = 0; j < kU; ++j) {
+                if (at[j] == -2) continue;
+                if (at[j] >= 0) {
+                    angles(at[j]);
+                    rotate<T, HALF>(u[j], v[j], w);
+                    if (HALF) v[j].store(op[j] + a.pairs);
                 }
-                u[j].set(x);
+                u[j].store(op[j]);
             }
         }
-#pragma unroll
-        for (int j = 0; j < kU; ++j) {
-            const int hj = h + j * step;
-            if (hj >= s.heads) continue;
-            u[j].store(op + hj * s.oh);
-            if (HALF && rotated) v[j].store(op + hj * s.oh + a.pairs);
+    } else {
+        // one token: this thread's column c, and its first head
+        const int part = (int)(local % (unsigned)parts);
+        int c, h;
+        bool on;
+        if (s.c_parts > 1) {
+            c = part % s.c_parts * kThreads + threadIdx.x;
+            h = part / s.c_parts;
+            on = c < s.row_items;
+        } else {
+            const int r = (int)threadIdx.x / s.row_items;
+            c = (int)threadIdx.x - r * s.row_items;
+            h = part * s.h_par + r;
+            on = r < s.h_par;
         }
-        h += kU * step;
+        if (!on) h = s.heads;
+        const int step = s.h_par * s.h_parts;
+        const unsigned b = tok0 / (unsigned)a.n_tok, t = tok0 % (unsigned)a.n_tok;
+        const bool rotated = c < s.rot;
+        const int e = element(c);
+        const T* xp = static_cast<const T*>(s.x) + b * s.xb + t * s.xt + e;
+        T* op = static_cast<T*>(s.out) + b * s.ob + t * s.ot + e;
+        auto load = [&]() {
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                const int hj = h + j * step;
+                if (hj >= s.heads) continue;
+                u[j].load(xp + hj * s.xh);
+                if (HALF && rotated) v[j].load(xp + hj * s.xh + a.pairs);
+            }
+        };
         load();
+        make_table(a, tok0, 1, cs);
+        if (on && rotated) angles(kA * c);
+        while (h < s.heads) {
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                const int hj = h + j * step;
+                if (hj >= s.heads) continue;
+                if (rotated) rotate<T, HALF>(u[j], v[j], w);
+                u[j].store(op + hj * s.oh);
+                if (HALF && rotated) v[j].store(op + hj * s.oh + a.pairs);
+            }
+            h += kU * step;
+            load();
+        }
     }
     // The attention kernels read their first query before they wait for this grid (they may, once all its
     // blocks have ended): the rows have reached L2 by then.  For the same reason there is no early
@@ -332,10 +367,13 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         } else if (s.row_items > kThreads) {
             s.c_parts = (s.row_items + kThreads - 1) / kThreads;
             most = s.heads;
-        } else if ((long long)s.heads * s.row_items <= kThreads / 2) {
+        } else if ((long long)s.heads * s.row_items <= kThreads && tokens > 1) {
+            // up to as many tokens as the table holds, while enough blocks remain to fill the SMs
             s.h_par = s.heads;
-            s.tokens = kThreads / (s.heads * s.row_items);
-            if (s.tokens > kTable / a.pairs) s.tokens = kTable / a.pairs;
+            s.tokens = kTable / a.pairs;
+            const long long even = (tokens + 2 * kNumSMs - 1) / (2 * kNumSMs);
+            const int room = kThreads / (s.heads * s.row_items);
+            if (s.tokens > even) s.tokens = (int)(even > room ? even : room < s.tokens ? room : s.tokens);
             if (s.tokens > tokens) s.tokens = (int)tokens;
             most = 1;
         } else {

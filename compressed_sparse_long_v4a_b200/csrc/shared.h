@@ -79,7 +79,6 @@ size_t shared_tc_workspace_bytes(const SharedArgs& a);
 cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t stream);
 
 // ---- attend_weights_tc.cu (tcgen05 path: bf16) ---------------------------
-bool weights_tc_shape_ok(const SharedArgs& a);
 cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t stream);
 
 }  // namespace v4a

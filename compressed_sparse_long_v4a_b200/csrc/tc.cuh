@@ -149,6 +149,10 @@ __device__ __forceinline__ void cp_async_16_hint(void* dst, const void* src, uin
                  "l"(policy)
                  : "memory");
 }
+// ... or 16 zero bytes (src is not read then, but has to be an address)
+__device__ __forceinline__ void cp_async_16_or_zero(void* dst, const void* src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
 // 4-byte copy global -> shared through L1 (completion tracked per thread by commit / wait groups)
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");

@@ -31,17 +31,16 @@ __device__ __forceinline__ float2 turn(double p, double f_hi, float f_lo) {
 inline void make_turns(int rope_dims, double base, Turns* t, double factor = 1, long long orig_ctx = 0, double beta_fast = 0,
                        double beta_slow = 0) {
     const long double two_pi = 6.283185307179586476925286766559005768L;
-    const long double step = powl((long double)base, -2.0L / rope_dims);
-    long double f = 1.0L;
+    const long double step = powl((long double)base, -2.0L / rope_dims), inv_factor = 1.0L / (long double)factor;
+    const long double span = 1.0L / ((long double)beta_fast - (long double)beta_slow);  // used with orig_ctx only
+    long double f = 1.0L / two_pi;  // turns
     for (int k = 0; k < rope_dims / 2; ++k, f *= step) {
-        long double g = f / (long double)factor;
+        long double g = f * inv_factor;
         if (orig_ctx > 0) {
-            const long double r = (long double)orig_ctx * f / two_pi;
-            long double w = (r - (long double)beta_slow) / ((long double)beta_fast - (long double)beta_slow);
+            long double w = ((long double)orig_ctx * f - (long double)beta_slow) * span;
             w = w < 0 ? 0 : w > 1 ? 1 : w;
             g = f * w + g * (1 - w);
         }
-        g /= two_pi;
         t->hi[k] = (double)g;
         t->lo[k] = (float)(g - (long double)t->hi[k]);
     }

@@ -487,8 +487,9 @@ typedef struct v4a_shared_cache {
  * query without candidates.  ext: as in the _ex calls, rotated at each
  * sequence's own positions.  Workspace: v4a_shared_workspace_size bytes,
  * 256-byte aligned.  Uses shape->batch, n_q, heads, d, m, window, ctx_len.
- * Errors as v4a_hca_attend, and V4A_ERR_INVALID_ARG for a prefix longer than
- * ctx_len / m. */
+ * Errors as v4a_hca_attend, V4A_ERR_INVALID_ARG for a prefix longer than
+ * ctx_len / m, and V4A_ERR_UNSUPPORTED for n_prefix + batch * (own_rows +
+ * window + n_q) >= 2^31. */
 V4A_API v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, void* out, v4a_dtype out_dtype,
                                          float* lse, v4a_dtype dtype, void* workspace, size_t workspace_bytes,
                                          int* dev_status, const v4a_attend_ext* ext, const v4a_shape* shape,
