@@ -597,6 +597,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
             }
             if (wait(&sm.p_free, j & 1)) {
                 tc::tc_fence_after();
+                const bool has = m_run != -INFINITY;  // the join does not read the others
                 float4* po = c.part_o + (pair + (long long)t.group) * (kRows * kD / 4) + rank * kHalf + r;
 #pragma unroll 1
                 for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
@@ -607,7 +608,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                     float4* pq = po + (long long)((q & ~1) + half) * 16 * kRows + (q & 1) * 8 * kRows;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        pq[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                        if (has) pq[k * kRows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                 }
                 tc::tc_fence_before();

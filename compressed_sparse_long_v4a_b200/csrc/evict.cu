@@ -170,9 +170,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             if (csize > 1) {
                 const uint32_t share = digits / csize;
                 if (threadIdx.x < share) {
-                    uint32_t c = 0;
-#pragma unroll 16
-                    for (int r = 0; r < csize; ++r) c += cluster.map_shared_rank(hist, r)[crank * share + threadIdx.x];
+                    uint32_t h[16], c = 0;  // all on their way together
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) h[r] = r < csize ? cluster.map_shared_rank(hist, r)[crank * share + threadIdx.x] : 0u;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) c += h[r];
                     sm.sums[pass][threadIdx.x] = c;
                 }
                 cluster.sync();
