@@ -271,8 +271,17 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_cons
         if (ml.x != -INFINITY) l += w[i] * ml.y;
     }
     l = block_reduce(l, red, false);  // behind its barriers every weight is written
-    if (a.sink && m != -INFINITY) l += exp2f(a.sink[h] * kLog2eF - m);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+    float keep = 1.f;
+    if (a.sink && m != -INFINITY) {
+        const float s = a.sink[h] * kLog2eF;
+        if (s > m && s < INFINITY) {  // the sink outweighs every key: it becomes the reference
+            keep = exp2f(m - s);
+            l *= keep;
+            m = s;
+        }
+        l += exp2f(s - m);
+    }
+    const float inv = l > 0.f ? keep / l : (l == 0.f ? 0.f : l);  // NaN stays
     if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
     for (int e = lane * 4; e < d; e += 128) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

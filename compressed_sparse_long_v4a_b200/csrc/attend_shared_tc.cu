@@ -101,6 +101,8 @@ struct PairArgs {
     int pre, own, win;     // tiles: prefix; own and window of a sequence (win: one more than the window fills, for a
                            // ring that wraps inside it)
     float scale_log2;
+    uint32_t polls;        // of a wait, before it gives up
+    int withhold;          // test hook (v4a_test_attend_fault): the tile of every pair whose loads are left out, or -1
     Range range[kPairs];
 };
 
@@ -249,18 +251,19 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
         more = walk.next(c, nxt);
         t.flags |= !more ? kLast | kEnd : nxt.flags & kFirst ? kLast : 0;
         if (t.flags & kFirst) {
-            if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1)) { ok = false; break; }
+            if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1, c.polls)) { ok = false; break; }
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
             tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
             ++piece;
         }
         // slabs 0-3, then 4-7: O is done with them one after the other
         for (int h = 0; h < 2; ++h) {
-            if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st][h], (j / kStages - 1) & 1)) { ok = false; break; }
+            if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st][h], (j / kStages - 1) & 1, c.polls)) { ok = false; break; }
             if (h == 0) {
                 sm.tile[st] = t;
                 tc::mbar_arrive(&sm.told[st]);
             }
+            if (j == c.withhold) continue;
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st][h], kXBytes);
             tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[t.kind], 0, t.y + (int)rank * kOwnKeys, 4 * h, t.b, x_full + 16 * st + 8 * h,
                                  t.kind == kPrefix ? again : once);
@@ -280,10 +283,10 @@ __device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, uint32_t r
     for (int j = 0;; ++j) {
         const int st = j % kStages;
         const uint32_t phase = (j / kStages) & 1;
-        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase)) { fault(sm, c, rank); return; }
+        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase, c.polls)) { fault(sm, c, rank); return; }
         const Tile t = sm.tile[st];
         if (t.flags & kNone) return;
-        if (!tc::mbar_wait(&sm.s_full[st], phase)) { fault(sm, c, rank); return; }
+        if (!tc::mbar_wait(&sm.s_full[st], phase, c.polls)) { fault(sm, c, rank); return; }
         tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
 #pragma unroll 1
         for (int u = 0; u < 4; ++u)
@@ -299,10 +302,10 @@ __device__ void pass_on_z(Smem& sm, const PairArgs& c) {
     for (int j = 0;; ++j) {
         const int st = j % kStages;
         const uint32_t phase = (j / kStages) & 1;
-        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase)) { fault(sm, c, 1); return; }
+        if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase, c.polls)) { fault(sm, c, 1); return; }
         const int flags = sm.tile[st].flags;
         if (flags & kNone) return;
-        if (!tc::mbar_wait(&sm.z_full[st], phase)) { fault(sm, c, 1); return; }
+        if (!tc::mbar_wait(&sm.z_full[st], phase, c.polls)) { fault(sm, c, 1); return; }
         tc::fence_proxy_async();
         tc::peer_arrive(ready + 8 * st);
         if (flags & kEnd) return;
@@ -319,8 +322,8 @@ __device__ void pass_on_z(Smem& sm, const PairArgs& c) {
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 constexpr uint32_t kAll = 0xffffffffu;
 
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-    for (uint32_t i = 0; i < tc::kWaitPolls; ++i)
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t polls) {
+    for (uint32_t i = 0; i < polls; ++i)
         if (__any_sync(kAll, tc::mbar_try_cluster(bar, parity))) return true;
     return false;
 }
@@ -330,19 +333,19 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
 __device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
     const uint32_t a0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.q), 16, 1024), b0 = (uint32_t)tc::sw128_desc(tc::smem_u32(sm.kv), 16, 1024);
     int pieces = 0;
-    bool ok = wait_cluster(&sm.x_full[0][0], 0);
+    bool ok = wait_cluster(&sm.x_full[0][0], 0, c.polls);
     int flags = ok ? sm.tile[0].flags : kNone;
     for (int j = 0; ok && !(flags & kNone); ++j) {
         const int st = j % kStages, st1 = (j + 1) % kStages;
         const uint32_t phase1 = (uint32_t)((j + 1) / kStages) & 1;
-        if (flags & kFirst) ok = wait_cluster(&sm.q_full, pieces++ & 1);
+        if (flags & kFirst) ok = wait_cluster(&sm.q_full, pieces++ & 1, c.polls);
         if (!ok) break;
         tc::tc_fence_after();
         uint32_t a = a0, b = b0 + st * (kXBytes >> 4);
         const uint32_t d = tmem + kColS + kColsS * st;
 #pragma unroll 1
         for (int s = 0; s < 8; ++s) {
-            if (s == 4 && !wait_cluster(&sm.x_full[st][1], (uint32_t)(j / kStages) & 1)) ok = false;
+            if (s == 4 && !wait_cluster(&sm.x_full[st][1], (uint32_t)(j / kStages) & 1, c.polls)) ok = false;
             if (s == 4) tc::tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) tc::mma_f16_pair(d, a + 2 * kk, b + 2 * kk, kDescHigh, kIdescQK, (uint32_t)(s | kk));
@@ -353,7 +356,7 @@ __device__ void issue_s(Smem& sm, const PairArgs& c, uint32_t tmem) {
         tc::mma_commit_pair(&sm.s_full[st]);
         if (flags & kLast) tc::mma_commit_pair(&sm.q_empty);
         if (flags & kEnd) break;
-        ok = wait_cluster(&sm.x_full[st1][0], phase1);
+        ok = wait_cluster(&sm.x_full[st1][0], phase1, c.polls);
         flags = sm.tile[st1].flags;
     }
     if (!ok) fault(sm, c, 0);
@@ -367,11 +370,11 @@ __device__ void issue_o(Smem& sm, const PairArgs& c, uint32_t tmem) {
     for (int j = 0;; ++j) {
         const int st = j % kStages;
         const uint32_t phase = (uint32_t)(j / kStages) & 1;
-        ok = wait_cluster(&sm.told[st], phase);
+        ok = wait_cluster(&sm.told[st], phase, c.polls);
         if (!ok) break;
         const int flags = sm.tile[st].flags;
         if (flags & kNone) break;
-        ok = wait_cluster(&sm.z_full[st], phase) && wait_cluster(&sm.z_ready[st], phase) && wait_cluster(&sm.p_full, (uint32_t)j & 1);
+        ok = wait_cluster(&sm.z_full[st], phase, c.polls) && wait_cluster(&sm.z_ready[st], phase, c.polls) && wait_cluster(&sm.p_full, (uint32_t)j & 1, c.polls);
         if (!ok) break;
         tc::tc_fence_after();
         uint32_t b = b0 + st * (kXBytes >> 4);
@@ -436,7 +439,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
     uint32_t mask = 0;  // of this thread's 32 keys
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (__all_sync(kAll, ok && tc::mbar_test(bar, parity))) return true;
-        if (ok) ok = tc::mbar_wait(bar, parity);
+        if (ok) ok = tc::mbar_wait(bar, parity, c.polls);
         ok = __all_sync(kAll, ok);
         return ok;
     };
@@ -751,7 +754,19 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
         }
         m = top;
     }
-    if (m != -INFINITY && a.sink) l += exp2f(a.sink[h] * kLog2eF - m);
+    if (m != -INFINITY && a.sink) {
+        const float s = a.sink[h] * kLog2eF;
+        if (s > m && s < INFINITY) {  // the sink outweighs every key: it becomes the reference
+            const float keep = exp2f(m - s);
+            l *= keep;
+            o.x *= keep;
+            o.y *= keep;
+            o.z *= keep;
+            o.w *= keep;
+            m = s;
+        }
+        l += exp2f(s - m);
+    }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
     if (a.lse && blockIdx.y == 0 && warp == 0 && row < c.rows)
         a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
@@ -831,6 +846,8 @@ void plan(const SharedArgs& a, PairArgs* c) {
     c->total = tiles_before(*c, c->groups);
     c->pairs = c->total < kPairs ? (int)c->total : kPairs;
     c->scale_log2 = kLog2eF / sqrtf((float)kD);
+    c->withhold = g_test_fault.withhold;
+    c->polls = c->withhold >= 0 ? g_test_fault.wait_polls : tc::kWaitPolls;
     // Equal shares of the work: the tiles, and kPiece for every piece (queries loaded, O written).  With many groups
     // a pair has many pieces anyway, and the tiles alone are shared out.
     constexpr int kPiece = 2;

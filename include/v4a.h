@@ -564,8 +564,9 @@ V4A_API int v4a_version(void);
 
 /* Fault injection for tests of the bounded waits (not part of the method;
  * never needed in normal use).  With withhold_tile >= 0, every later launch
- * of the tensor-core attention kernel (the bf16, d = 512, 64-head path of
- * the CSA and HCA attention calls) makes each CTA skip the copies of its
+ * of the tensor-core attention kernels (the bf16, d = 512, 64-head path of
+ * the CSA and HCA attention calls, and the bf16, d = 512 path of
+ * v4a_hca_attend_shared) makes each CTA skip the copies of its
  * local tile withhold_tile -- no copy is issued and no arrival made, so that
  * stage never fills -- and gives every wait of the kernel wait_polls polls
  * (each suspends for at most ~20 us) and the MMA warp ~2 ms without progress.
