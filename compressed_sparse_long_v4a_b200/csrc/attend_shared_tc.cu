@@ -90,6 +90,8 @@ struct Range {
     int last;      // group of the last one
 };
 
+constexpr int kSpans = 256;
+
 struct PairArgs {
     SharedArgs a;
     float2* part_ml;       // [pieces][128] (m in base-2 logits, l); piece = pair + group
@@ -104,6 +106,7 @@ struct PairArgs {
     uint32_t polls;        // of a wait, before it gives up
     int withhold;          // test hook (v4a_test_attend_fault): the tile of every pair whose loads are left out, or -1
     Range range[kPairs];
+    struct { unsigned char first, n; } span[kSpans];  // the pairs that have tiles of a group, for the first groups
 };
 
 // Tiles of the groups before g (host).  A group has `pre` tiles and own + win for every sequence with rows in it: one
@@ -114,6 +117,18 @@ long long tiles_before(const PairArgs& c, int g) {
     const unsigned last = (unsigned)(e < c.rows ? e : c.rows) - 1;
     const long long seqs = g + (long long)(last / c.per_seq) - (long long)(last / c.lcm);
     return (long long)g * c.pre + seqs * (c.own + c.win);
+}
+
+// The pairs that have tiles of group g: from the last one that begins no later than its first tile to the last that begins
+// no later than its last.
+__host__ __device__ inline void find_pairs(const PairArgs& c, int g, int* first, int* n) {
+    int p0 = 0, p1 = 0;
+    for (int k = 64; k > 0; k >>= 1) {
+        if (p0 + k < c.pairs && (c.range[p0 + k].g < g || (c.range[p0 + k].g == g && c.range[p0 + k].i == 0))) p0 += k;
+        if (p1 + k < c.pairs && c.range[p1 + k].g <= g) p1 += k;
+    }
+    *first = p0;
+    *n = c.pairs > 0 ? p1 - p0 + 1 : 0;
 }
 
 // walks the tiles of a range that hold anything
@@ -235,11 +250,30 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
     Tile t, nxt;
     int j = 0, piece = 0;
     bool ok = true, more = true;
-    // what can be done before the kernel before this one has finished: a prefix tile depends on sizes alone
+    // What can be done before the kernel before this one has finished: a prefix tile depends on sizes alone.  Its loads
+    // are the first thing then (the barriers complete only once their bytes are announced below).
     const bool early = c.range[pair].i < c.pre;
+    auto load = [&](const Tile& tile, int st, int h) {
+        tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[tile.kind], 0, tile.y + (int)rank * kOwnKeys, 4 * h, tile.b, x_full + 16 * st + 8 * h,
+                             tile.kind == kPrefix ? again : once);
+    };
+    auto load_q = [&](const Tile& tile) {
+        tc::tma_load_4d_pair(sm.q, &maps.q, 0, tile.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
+    };
+    tc::prefetch_map(&maps.q);
+    tc::prefetch_map(&maps.x[kPrefix]);
+    tc::prefetch_map(&maps.z[kPrefix]);
     if (early) walk.next(c, t);
     griddep_wait();
-    if (!early) more = walk.next(c, t);
+    if (early) {
+        load_q(t);
+        if (c.withhold != 0) {
+            load(t, 0, 0);
+            load(t, 0, 1);
+        }
+    } else {
+        more = walk.next(c, t);
+    }
     if (!more) {
         sm.tile[0].flags = kNone;
         tc::mbar_arrive(&sm.told[0]);
@@ -253,7 +287,7 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
         if (t.flags & kFirst) {
             if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1, c.polls)) { ok = false; break; }
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
-            tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
+            if (j > 0 || !early) load_q(t);
             ++piece;
         }
         // slabs 0-3, then 4-7: O is done with them one after the other
@@ -265,8 +299,7 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
             }
             if (j == c.withhold) continue;
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st][h], kXBytes);
-            tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[t.kind], 0, t.y + (int)rank * kOwnKeys, 4 * h, t.b, x_full + 16 * st + 8 * h,
-                                 t.kind == kPrefix ? again : once);
+            if (j > 0 || !early) load(t, st, h);
         }
         if (!ok) break;
     }
@@ -522,20 +555,23 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         // The weights are taken against the maximum so far.  Where that was too low for some row, the four threads of each row agree on
         // a new one and take them again: at the start of a piece, hardly ever later.
         uint32_t pk[16];
-        float ls[2], alpha = 1.f;
+        float ls[2] = {0.f, 0.f}, alpha = 1.f;
         bool leave = false, settled = false;
+        const bool fresh = t.flags & kFirst;  // nothing to take them against yet
 #pragma unroll 1
         for (;;) {
-            const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
-            ls[0] = ls[1] = 0.f;
+            if (!fresh || settled) {
+                const float sub_m = m_run == -INFINITY ? 0.f : m_run;  // nothing seen so far: every x is -inf
+                ls[0] = ls[1] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
-                ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
-                const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-                pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+                for (int k = 0; k < 16; ++k) {
+                    const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
+                    ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
+                    const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+                    pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+                }
             }
-            if (settled || !tc::named_barrier_or(1, 256, mt > m_run + kSlack || odd || !ok)) break;
+            if (settled || !tc::named_barrier_or(1, 256, fresh || mt > m_run + kSlack || odd || !ok)) break;
             settled = true;
             sm.mx[quarter][r] = mt;
             leave = tc::named_barrier_or(1, 256, !ok);
@@ -705,15 +741,13 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
         live = has_candidates(a, pos);
         if (blockIdx.y == 0 && warp == 0 && h == 0 && query % (unsigned)a.n_q == 0) report_sequence(a, b);
     }
-    // pieces of this group: pairs p0 .. p1, the last ones that begin no later than its first, and its last, tile
+    // pieces of this group: pairs p0 .. p0 + n - 1
     int p0 = 0, n = 0;
-    if (c.pairs > 0) {
-        int p1 = 0;
-        for (int k = 64; k > 0; k >>= 1) {
-            if (p0 + k < c.pairs && (c.range[p0 + k].g < g || (c.range[p0 + k].g == g && c.range[p0 + k].i == 0))) p0 += k;
-            if (p1 + k < c.pairs && c.range[p1 + k].g <= g) p1 += k;
-        }
-        n = p1 - p0 + 1;
+    if (g < kSpans) {
+        p0 = c.span[g].first;
+        n = c.span[g].n;
+    } else {
+        find_pairs(c, g, &p0, &n);
     }
     const float2* ml = c.part_ml + (long long)(p0 + g) * kRows + rg;
     const float4* po = c.part_o + (long long)(p0 + g) * (kRows * kD / 4) + quad * kRows + rg;
@@ -886,6 +920,12 @@ void plan(const SharedArgs& a, PairArgs* c) {
         pairs = p + 1;
     }
     c->pairs = pairs;
+    for (int k = 0; k < c->groups && k < kSpans; ++k) {
+        int first, n;
+        find_pairs(*c, k, &first, &n);
+        c->span[k].first = (unsigned char)first;
+        c->span[k].n = (unsigned char)n;
+    }
 }
 long long pieces(const PairArgs& c) { return c.total > 0 ? (long long)c.groups + c.pairs - 1 : 0; }
 
