@@ -4,12 +4,13 @@
 //     out = sum_r p_r v_r,  p = softmax_r(q . v_r / sqrt(d)),  lse = log sum_r e^{q . v_r / sqrt(d)}
 //
 // Every query of the batch sees the whole prefix, so the rows (sequence, query, head) of all sequences are
-// one matrix, taken in groups of 128 that ignore where a sequence ends.  A group's keys are tiles of 128:
+// one matrix, taken in groups of 128 that ignore where a sequence ends.  A group's keys come in boxes of 64:
 // the prefix, then the own slots and the window of each sequence that has rows in the group; rows of
-// other sequences are masked there.  The tiles of all groups form one flat sequence, cut into equal ranges.
+// other sequences are masked there.  The boxes of all groups form one flat sequence, cut into equal ranges;
+// two boxes that hold anything, of whatever kind, make a tile of 128 keys.
 //
 // A range goes to a CTA pair (two SMs, cta_group::2), each CTA holding 64 of the 128 rows.  Per tile
-//     S  = Q K^T   M = 128 rows x N = 128 keys x K = 512   (each CTA brings 64 of the keys)
+//     S  = Q K^T   M = 128 rows x N = 128 keys x K = 512   (each CTA brings a box of 64 of the keys)
 //     P  = softmax(S), four threads per row, lazily rescaled maximum
 //     O += P V     M = 128 x N = 2 x 256 dims x K = 128 keys (each CTA brings half of the dims)
 // With 64 rows of 512 dims a CTA's O is half of tensor memory, and 64 rows at the full rate of the tensor
@@ -47,27 +48,30 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRows = 128;          // rows of a group
 constexpr int kHalf = 64;           // ... of one CTA
-constexpr int kKeys = 128;          // keys of a tile
-constexpr int kOwnKeys = 64;        // ... of which a CTA brings these for S
+constexpr int kBox = 64;            // keys of a box, which one load brings
+constexpr int kKeys = 2 * kBox;     // keys of a tile: a box per CTA
 constexpr int kStages = 2;          // and S buffers
 constexpr int kPairs = kNumSMs / 2;
-constexpr uint32_t kXBytes = kOwnKeys * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
-constexpr uint32_t kSlab = kOwnKeys * 128;  // 64 dims of a CTA's keys
+constexpr uint32_t kXBytes = kBox * kD * 2, kZBytes = kXBytes / 2, kQBytes = kHalf * kD * 2;
+constexpr uint32_t kSlab = kBox * 128;  // 64 dims of a CTA's keys
 constexpr uint32_t kColS = 256, kColsS = 64, kTmemCols = 512;  // O: columns 0-255
 constexpr int kThreads = 12 * 32;
 constexpr float kSlack = 8.0f;           // keep a stale running max until the true one exceeds it by 2^8
 constexpr uint32_t kIdescQK = tc::idesc_f16(128, kKeys, 0, 0), kIdescPV = tc::idesc_f16(128, 256, 0, 1);
 
 enum Kind { kPrefix, kOwn, kWindow };
-// first, last: of its piece; end: last of the range; none: the range holds nothing; same: a full tile of the
-// prefix behind another one
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kNone = 8, kSame = 16 };
+// first, last: of its piece; end: last of the range; none: the range holds nothing; plain: of the prefix alone; same: a
+// full tile of the prefix behind another one
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kNone = 8, kPlain = 16, kSame = 32 };
 
-struct __align__(16) Tile {
-    int flags, kind;
-    int group, b;        // b: the sequence (own, window)
-    int y, n;            // first row of its 128 in prefix / own / ring, rows that count
+struct Box {
+    int kind, b;         // b: the sequence (own, window)
+    int y, n;            // first row of its 64 in prefix / own / ring, rows that count
     long long p0;        // what row y holds: own slot, or position
+};
+struct __align__(16) Tile {
+    int flags, group;
+    Box box[2];          // of CTA 0, which are keys 0-63, and of CTA 1
 };
 
 struct __align__(1024) Smem {
@@ -86,7 +90,7 @@ struct __align__(1024) Smem {
 };
 
 struct Range {
-    int g, i, n;   // a pair's first tile: its group and its place in it; how many tiles
+    int g, i, n;   // a pair's first box: its group and its place in it; how many boxes
     int last;      // group of the last one
 };
 
@@ -96,22 +100,22 @@ struct PairArgs {
     SharedArgs a;
     float2* part_ml;       // [pieces][128] (m in base-2 logits, l); piece = pair + group
     float4* part_o;        // [pieces][128 quads of dims][128 rows]
-    long long total;       // tiles of all groups
+    long long total;       // boxes of all groups
     unsigned rows, per_seq, lcm;  // batch * n_q * heads; n_q * heads; least common multiple of that and 128
     int groups, pairs;
-    int pre_tail;          // keys of the prefix's last tile
-    int pre, own, win;     // tiles: prefix; own and window of a sequence (win: one more than the window fills, for a
+    int pre_tail;          // keys of the prefix's last box
+    int pre, own, win;     // boxes: prefix; own and window of a sequence (win: one more than the window fills, for a
                            // ring that wraps inside it)
     float scale_log2;
     uint32_t polls;        // of a wait, before it gives up
     int withhold;          // test hook (v4a_test_attend_fault): the tile of every pair whose loads are left out, or -1
     Range range[kPairs];
-    struct { unsigned char first, n; } span[kSpans];  // the pairs that have tiles of a group, for the first groups
+    struct { unsigned char first, n; } span[kSpans];  // the pairs that have boxes of a group, for the first groups
 };
 
-// Tiles of the groups before g (host).  A group has `pre` tiles and own + win for every sequence with rows in it: one
+// Boxes of the groups before g (host).  A group has `pre` boxes and own + win for every sequence with rows in it: one
 // more than the sequences that begin inside it, behind its first row.
-long long tiles_before(const PairArgs& c, int g) {
+long long boxes_before(const PairArgs& c, int g) {
     if (g == 0) return 0;
     const unsigned long long e = (unsigned long long)g * kRows;
     const unsigned last = (unsigned)(e < c.rows ? e : c.rows) - 1;
@@ -119,7 +123,7 @@ long long tiles_before(const PairArgs& c, int g) {
     return (long long)g * c.pre + seqs * (c.own + c.win);
 }
 
-// The pairs that have tiles of group g: from the last one that begins no later than its first tile to the last that begins
+// The pairs that have boxes of group g: from the last one that begins no later than its first box to the last that begins
 // no later than its last.
 __host__ __device__ inline void find_pairs(const PairArgs& c, int g, int* first, int* n) {
     int p0 = 0, p1 = 0;
@@ -131,11 +135,11 @@ __host__ __device__ inline void find_pairs(const PairArgs& c, int g, int* first,
     *n = c.pairs > 0 ? p1 - p0 + 1 : 0;
 }
 
-// walks the tiles of a range that hold anything
+// walks the boxes of a range that hold anything
 struct Walk {
-    int left, g, i, per;        // tiles to go; group, tile in it, its tiles
-    int s, w;                   // sequence and its tile
-    bool fresh, entered;        // no tile of this group yet; the sequence's numbers are read
+    int left, g, i, per;        // boxes to go; group, box in it, its boxes
+    int s, w;                   // sequence and its box
+    bool entered;               // the sequence's numbers are read
     int count, row0, n_a, n_w;  // own slots; window: ring row of position lo, positions before the ring's end, all
     long long lo;
 
@@ -143,7 +147,6 @@ struct Walk {
         const unsigned r0 = (unsigned)g * kRows, r1 = min(r0 + kRows, c.rows) - 1;
         s = (int)(r0 / c.per_seq);
         per = c.pre + ((int)(r1 / c.per_seq) - s + 1) * (c.own + c.win);
-        fresh = true;
         entered = false;
         w = 0;
     }
@@ -168,7 +171,7 @@ struct Walk {
             w = k % (c.own + c.win);
         }
     }
-    __device__ bool next(const PairArgs& c, Tile& t) {
+    __device__ bool next(const PairArgs& c, Box& t, int& group) {
         while (left > 0) {
             if (i == per) {
                 ++g;
@@ -176,14 +179,13 @@ struct Walk {
                 enter_group(c);
             }
             --left;
-            bool live = true, same = false;
+            group = g;
             if (i < c.pre) {
                 t.kind = kPrefix;
-                t.y = i * kKeys;
-                t.n = i + 1 == c.pre ? c.pre_tail : kKeys;
+                t.y = i * kBox;
+                t.n = i + 1 == c.pre ? c.pre_tail : kBox;
                 t.b = 0;
                 t.p0 = t.y;
-                same = !fresh && t.n == kKeys;  // every tile before it in its piece was one
                 ++i;
             } else {
                 if (!entered) enter_sequence(c);
@@ -191,25 +193,24 @@ struct Walk {
                 t.b = s;
                 if (w < c.own) {
                     t.kind = kOwn;
-                    t.y = w * kKeys;
+                    t.y = w * kBox;
                     t.p0 = t.y;
-                    t.n = min(count - t.y, kKeys);
+                    t.n = min(count - t.y, kBox);
                 } else {
-                    int at = (w - c.own) * kKeys;
-                    const int a_rows = (n_a + kKeys - 1) / kKeys * kKeys;
+                    int at = (w - c.own) * kBox;
+                    const int a_rows = (n_a + kBox - 1) / kBox * kBox;
                     t.kind = kWindow;
                     if (at < a_rows) {
                         t.y = row0 + at;
                         t.p0 = lo + at;
-                        t.n = min(n_a - at, kKeys);
+                        t.n = min(n_a - at, kBox);
                     } else {
                         at -= a_rows;
                         t.y = at;
                         t.p0 = lo + n_a + at;
-                        t.n = min(n_w - n_a - at, kKeys);
+                        t.n = min(n_w - n_a - at, kBox);
                     }
                 }
-                live = t.n > 0;
                 ++i;
                 if (++w == c.own + c.win) {
                     w = 0;
@@ -217,12 +218,7 @@ struct Walk {
                     entered = false;
                 }
             }
-            if (live) {
-                t.group = g;
-                t.flags = (fresh ? kFirst : 0) | (same ? kSame : 0);
-                fresh = false;
-                return true;
-            }
+            if (t.n > 0) return true;
         }
         return false;
     }
@@ -247,61 +243,88 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
     const uint64_t again = tc::l2_evict_normal(), once = tc::l2_stream_policy((int)((c.per_seq + kRows - 1) / kRows));
     const uint32_t x_full = tc::peer_addr(&sm.x_full[0][0], 0), q_full = tc::peer_addr(&sm.q_full, 0);
     Walk walk(c, pair);
-    Tile t, nxt;
-    int j = 0, piece = 0;
-    bool ok = true, more = true;
-    // What can be done before the kernel before this one has finished: a prefix tile depends on sizes alone.  Its loads
-    // are the first thing then (the barriers complete only once their bytes are announced below).
-    const bool early = c.range[pair].i < c.pre;
-    auto load = [&](const Tile& tile, int st, int h) {
-        tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[tile.kind], 0, tile.y + (int)rank * kOwnKeys, 4 * h, tile.b, x_full + 16 * st + 8 * h,
-                             tile.kind == kPrefix ? again : once);
+    Tile t;
+    Box nxt;  // the box behind the tile's
+    int piece = 0, group = -1, nxt_group = 0;
+    bool ok = true, more = true, plain = false;
+    auto load = [&](int st, int h) {
+        const Box& x = t.box[rank];
+        tc::tma_load_4d_pair(sm.kv[st] + 4 * kSlab * h, &maps.x[x.kind], 0, x.y, 4 * h, x.b, x_full + 16 * st + 8 * h,
+                             x.kind == kPrefix ? again : once);
     };
-    auto load_q = [&](const Tile& tile) {
-        tc::tma_load_4d_pair(sm.q, &maps.q, 0, tile.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
+    auto load_q = [&] {
+        tc::tma_load_4d_pair(sm.q, &maps.q, 0, t.group * kRows + (int)rank * kHalf, 0, 0, q_full, again);
     };
+    auto set_flags = [&] {  // with the box behind the tile known
+        const bool first = t.group != group, all = t.box[0].kind == kPrefix && t.box[1].kind == kPrefix;
+        const bool full = all && t.box[0].n == kBox && t.box[1].n == kBox;
+        t.flags = (first ? kFirst : 0) | (!more ? kLast | kEnd : nxt_group != t.group ? kLast : 0) | (all ? kPlain : 0) |
+                  (full && plain && !first ? kSame : 0);
+        group = t.group;
+        plain = full;
+    };
+    auto next_tile = [&] {  // two boxes of one group, or the last one and an empty one (rows beyond every array: zeros)
+        t.group = nxt_group;
+        t.box[0] = t.box[1] = nxt;
+        t.box[1].n = 0;
+        t.box[1].y = 0x3fffffff;
+        more = walk.next(c, nxt, nxt_group);
+        if (more && nxt_group == t.group) {
+            t.box[1] = nxt;
+            more = walk.next(c, nxt, nxt_group);
+        }
+        set_flags();
+    };
+    // What can be done before the kernel before this one has finished: a tile of the prefix depends on sizes alone.  Its
+    // loads are the first thing then (the barriers complete only once their bytes are announced below).
+    const bool early = c.range[pair].i + 1 < c.pre && c.range[pair].n > 1;
     tc::prefetch_map(&maps.q);
     tc::prefetch_map(&maps.x[kPrefix]);
     tc::prefetch_map(&maps.z[kPrefix]);
-    if (early) walk.next(c, t);
+    if (early) {
+        walk.next(c, t.box[0], t.group);
+        walk.next(c, t.box[1], t.group);
+    }
     griddep_wait();
     if (early) {
-        load_q(t);
+        load_q();
         if (c.withhold != 0) {
-            load(t, 0, 0);
-            load(t, 0, 1);
+            load(0, 0);
+            load(0, 1);
         }
+        more = walk.next(c, nxt, nxt_group);
+        set_flags();
+    } else if (walk.next(c, nxt, nxt_group)) {
+        next_tile();
     } else {
-        more = walk.next(c, t);
-    }
-    if (!more) {
+        t.flags = kNone;
         sm.tile[0].flags = kNone;
         tc::mbar_arrive(&sm.told[0]);
         if (rank == 0) tc::mbar_arrive(&sm.x_full[0][0]);
     }
-    for (; more; t = nxt, ++j) {
+    for (int j = 0; !(t.flags & kNone); ++j) {
         const int st = j % kStages;
-        if (aborted(sm)) { ok = false; break; }
-        more = walk.next(c, nxt);
-        t.flags |= !more ? kLast | kEnd : nxt.flags & kFirst ? kLast : 0;
-        if (t.flags & kFirst) {
-            if (piece > 0 && !tc::mbar_wait(&sm.q_empty, (piece - 1) & 1, c.polls)) { ok = false; break; }
-            if (rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
-            if (j > 0 || !early) load_q(t);
+        if (aborted(sm)) ok = false;
+        if (ok && (t.flags & kFirst)) {
+            if (piece > 0) ok = tc::mbar_wait(&sm.q_empty, (piece - 1) & 1, c.polls);
+            if (ok && rank == 0) tc::mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
+            if (ok && (j > 0 || !early)) load_q();
             ++piece;
         }
         // slabs 0-3, then 4-7: O is done with them one after the other
-        for (int h = 0; h < 2; ++h) {
-            if (j >= kStages && !tc::mbar_wait(&sm.kv_empty[st][h], (j / kStages - 1) & 1, c.polls)) { ok = false; break; }
+        for (int h = 0; ok && h < 2; ++h) {
+            if (j >= kStages) ok = tc::mbar_wait(&sm.kv_empty[st][h], (j / kStages - 1) & 1, c.polls);
+            if (!ok) break;
             if (h == 0) {
                 sm.tile[st] = t;
                 tc::mbar_arrive(&sm.told[st]);
             }
             if (j == c.withhold) continue;
             if (rank == 0) tc::mbar_arrive_expect_tx(&sm.x_full[st][h], kXBytes);
-            if (j > 0 || !early) load(t, st, h);
+            if (j > 0 || !early) load(st, h);
         }
-        if (!ok) break;
+        if (!ok || (t.flags & kEnd)) break;
+        next_tile();
     }
     if (!ok) {  // what was asked for lands long before this ends
         fault(sm, c, rank);
@@ -317,15 +340,15 @@ __device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, uint32_t r
         const int st = j % kStages;
         const uint32_t phase = (j / kStages) & 1;
         if (aborted(sm) || !tc::mbar_wait(&sm.told[st], phase, c.polls)) { fault(sm, c, rank); return; }
-        const Tile t = sm.tile[st];
-        if (t.flags & kNone) return;
+        const int flags = sm.tile[st].flags;
+        if (flags & kNone) return;
+        const Box z = sm.tile[st].box[other];
         if (!tc::mbar_wait(&sm.s_full[st], phase, c.polls)) { fault(sm, c, rank); return; }
         tc::mbar_arrive_expect_tx(&sm.z_full[st], kZBytes);
 #pragma unroll 1
         for (int u = 0; u < 4; ++u)
-            tc::tma_load_4d(sm.kv[st] + kSlab * (2 * u + other), &maps.z[t.kind], 0, t.y + (int)other * kOwnKeys, 2 * u + (int)rank, t.b,
-                            &sm.z_full[st], again);
-        if (t.flags & kEnd) return;
+            tc::tma_load_4d(sm.kv[st] + kSlab * (2 * u + other), &maps.z[z.kind], 0, z.y, 2 * u + (int)rank, z.b, &sm.z_full[st], again);
+        if (flags & kEnd) return;
     }
 }
 
@@ -457,7 +480,6 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
     // four warps take the second 32 of those keys.  So four threads share a row, each a quarter of the keys.
     const int sub = (threadIdx.x >> 5) & 3, wg = (threadIdx.x - 64) >> 7;
     const int lane = threadIdx.x & 31, half = sub >> 1, r = 32 * (sub & 1) + lane, quarter = 2 * half + wg;
-    const int key0 = 32 * quarter;
     const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
     const uint32_t p_full = tc::peer_addr(&sm.p_full, 0);
     uint8_t* const prow = sm.p[half] + (r >> 3) * 1024 + (r & 7) * 128;
@@ -480,16 +502,16 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
     for (int j = 0;; ++j) {
         const int st = j % kStages;
         const uint32_t phase = (j / kStages) & 1;
-        Tile t;
-        t.flags = kSame;
-        t.kind = kPrefix;
-        t.group = first_group;
-        if (wait(&sm.told[st], phase)) t = sm.tile[st];
-        if (t.flags & kNone) break;
-        if (t.flags & kFirst) {
+        int flags = kSame | kPlain, group = first_group;
+        if (wait(&sm.told[st], phase)) {
+            flags = sm.tile[st].flags;
+            group = sm.tile[st].group;
+        }
+        if (flags & kNone) break;
+        if (flags & kFirst) {
             m_run = -INFINITY;
             l_run = 0.f;
-            const unsigned row = (unsigned)t.group * kRows + rank * kHalf + r;
+            const unsigned row = (unsigned)group * kRows + rank * kHalf + r;
             alive = row < c.rows;
             if (alive) {
                 const unsigned query = row / (unsigned)a.heads;
@@ -499,9 +521,10 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 seen = seen_entries(a, pos);
             }
         }
-        if (!(t.flags & kSame)) {
+        if (!(flags & kSame)) {
+            const Box t = sm.tile[st].box[half];
             mask = alive ? ~0u : 0u;
-            const int n = t.n - key0;
+            const int key0 = 32 * wg, n = t.n - key0;
             if (t.kind == kPrefix) {
                 mask &= low_bits(n);
             } else if (t.kind == kOwn) {
@@ -538,7 +561,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
             for (int k = 0; k < 32; ++k) x[k] = 0.f;
         }
         bool odd = false;  // a key of this tile is not finite
-        if (t.kind != kPrefix) {
+        if (!(flags & kPlain)) {
             float d = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k) d = fmaf(x[k], 0.f, d);
@@ -557,7 +580,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         uint32_t pk[16];
         float ls[2] = {0.f, 0.f}, alpha = 1.f;
         bool leave = false, settled = false;
-        const bool fresh = t.flags & kFirst;  // nothing to take them against yet
+        const bool fresh = flags & kFirst;  // nothing to take them against yet
 #pragma unroll 1
         for (;;) {
             if (!fresh || settled) {
@@ -623,21 +646,21 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
         __syncwarp();
         if (lane == 0 && ok) tc::peer_arrive(p_full);
 
-        if (t.flags & kLast) {
+        if (flags & kLast) {
             // write the piece
-            for (; next_group < t.group; ++next_group)  // groups of the range without a tile that holds anything
+            for (; next_group < group; ++next_group)  // groups of the range without a box that holds anything
                 if (quarter == 0) ml(next_group) = make_float2(-INFINITY, 0.f);
             ++next_group;
             sm.ls[quarter][r] = l_run;
             tc::named_barrier(1, 256);
             if (quarter == 0) {
                 const float l = (l_run + sm.ls[1][r]) + (sm.ls[2][r] + sm.ls[3][r]);
-                ml(t.group) = make_float2(isnan(l) ? NAN : m_run, l);
+                ml(group) = make_float2(isnan(l) ? NAN : m_run, l);
             }
             if (wait(&sm.p_free, j & 1)) {
                 tc::tc_fence_after();
                 const bool has = m_run != -INFINITY;  // the join does not read the others
-                float4* po = c.part_o + (pair + (long long)t.group) * (kRows * kD / 4) + rank * kHalf + r;
+                float4* po = c.part_o + (pair + (long long)group) * (kRows * kD / 4) + rank * kHalf + r;
 #pragma unroll 1
                 for (int q = 4 * wg; q < 4 * wg + 4; ++q) {
                     uint32_t o[32];
@@ -653,7 +676,7 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 tc::tc_fence_before();
             }
         }
-        if (t.flags & kEnd) break;
+        if (flags & kEnd) break;
     }
     for (; next_group <= last_group; ++next_group)
         if (quarter == 0) ml(next_group) = make_float2(-INFINITY, 0.f);
@@ -873,18 +896,18 @@ void plan(const SharedArgs& a, PairArgs* c) {
     const unsigned long long lcm = (unsigned long long)(c->per_seq / x) * kRows;
     c->lcm = lcm < 0xffffffffULL ? (unsigned)lcm : 0xffffffffu;  // beyond every row: divides to 0 either way
     c->groups = (int)((c->rows + kRows - 1) / kRows);
-    c->pre = (int)((a.n_prefix + kKeys - 1) / kKeys);
-    c->pre_tail = (int)(a.n_prefix - (long long)(c->pre - 1) * kKeys);
-    c->own = (a.own_rows + kKeys - 1) / kKeys;
-    c->win = a.window > 0 ? (int)(((long long)a.window + a.n_q - 1 + kKeys - 1) / kKeys) + 1 : 0;
-    c->total = tiles_before(*c, c->groups);
-    c->pairs = c->total < kPairs ? (int)c->total : kPairs;
+    c->pre = (int)((a.n_prefix + kBox - 1) / kBox);
+    c->pre_tail = (int)(a.n_prefix - (long long)(c->pre - 1) * kBox);
+    c->own = (a.own_rows + kBox - 1) / kBox;
+    c->win = a.window > 0 ? (int)(((long long)a.window + a.n_q - 1 + kBox - 1) / kBox) + 1 : 0;
+    c->total = boxes_before(*c, c->groups);
+    c->pairs = (c->total + 1) / 2 < kPairs ? (int)((c->total + 1) / 2) : kPairs;
     c->scale_log2 = kLog2eF / sqrtf((float)kD);
     c->withhold = g_test_fault.withhold;
     c->polls = c->withhold >= 0 ? g_test_fault.wait_polls : tc::kWaitPolls;
-    // Equal shares of the work: the tiles, and kPiece for every piece (queries loaded, O written).  With many groups
-    // a pair has many pieces anyway, and the tiles alone are shared out.
-    constexpr int kPiece = 2;
+    // Equal shares of the work: the boxes, and kPiece for every piece (queries loaded, O written).  With many groups
+    // a pair has many pieces anyway, and the boxes alone are shared out.
+    constexpr int kPiece = 4;
     const int extra = c->groups <= 8 * kPairs ? kPiece : 0;
     const long long cost = c->total + (long long)extra * (c->groups + c->pairs - 1);
     long long f = 0;
@@ -897,7 +920,7 @@ void plan(const SharedArgs& a, PairArgs* c) {
             f1 = (p + 1) * c->total / c->pairs;
         } else {
             for (budget -= extra; budget > 0 && f1 < c->total;) {
-                const long long end = tiles_before(*c, h + 1), n = end - f1 < budget ? end - f1 : budget;
+                const long long end = boxes_before(*c, h + 1), n = end - f1 < budget ? end - f1 : budget;
                 f1 += n;
                 budget -= n;
                 if (f1 == end) {
@@ -905,18 +928,21 @@ void plan(const SharedArgs& a, PairArgs* c) {
                     budget -= extra;
                 }
             }
-            if (f1 == f) f1 = f + 1;
             if (p == c->pairs - 1) f1 = c->total;
         }
-        while (g + 1 < c->groups && tiles_before(*c, g + 1) <= f) ++g;
+        // whole tiles of a group
+        for (h = g; h + 1 < c->groups && boxes_before(*c, h + 1) <= f1;) ++h;
+        if (f1 < c->total && ((f1 - boxes_before(*c, h)) & 1)) --f1;
+        if (f1 <= f) f1 = f + 2 < boxes_before(*c, g + 1) ? f + 2 : boxes_before(*c, g + 1);
+        while (g + 1 < c->groups && boxes_before(*c, g + 1) <= f) ++g;
         Range& r = c->range[p];
         r.g = g;
-        r.i = (int)(f - tiles_before(*c, g));
+        r.i = (int)(f - boxes_before(*c, g));
         r.n = (int)(f1 - f);
         if (p > 0) c->range[p - 1].last = r.i > 0 ? g : g - 1;
         r.last = c->groups - 1;
         f = f1;
-        while (g + 1 < c->groups && tiles_before(*c, g + 1) <= f) ++g;
+        while (g + 1 < c->groups && boxes_before(*c, g + 1) <= f) ++g;
         pairs = p + 1;
     }
     c->pairs = pairs;
@@ -953,8 +979,8 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
         bool ok = make_map(&maps.q, a.q, 1, c.rows, kHalf, 8);
         for (int k = 0; k < 3; ++k) {
             const bool have = in[k].p && in[k].rows > 0;  // without: no tile asks for it
-            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 4) &&
-                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kOwnKeys, 1);
+            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kBox, 4) &&
+                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kBox, 1);
         }
         if (!ok) return cudaErrorNotSupported;
         const size_t smem = sizeof(Smem) + 1024;
