@@ -1,6 +1,6 @@
 // attend_shared.cu -- HCA attention over a prefix that a batch shares, entries of each sequence's own and the
 // window, and the weights that the own entries receive: entry points, and the CUDA-core kernels
-// (fp32, and shapes that the tensor-core kernels do not take).
+// (fp32; attention also bf16 with d < 512).
 //
 //     out = sum_r p_r v_r,  p = softmax_r(q . v_r / sqrt(d)),  lse = log sum_r e^{q . v_r / sqrt(d)}
 //
@@ -12,9 +12,11 @@
 // end: out = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i.
 //
 // CUDA-core kernels: a block takes 16 rows (4 per warp) and tiles of 32 keys staged as fp32 in shared
-// memory.  For the scores a lane is a key; for the output it is a slice of d, and each probability is
-// broadcast from the lane that has it.  4 rows per warp mean 16 FMAs per 16-byte read of a key, which the
-// FMA pipes bound.  Products and sums in fp32 throughout.
+// memory (fp32 by asynchronous copies, all of a tile in flight).  For the scores a lane is a key; for the output it is a
+// slice of d, and each probability is broadcast from the lane that has it.  4 rows per warp mean 16 FMAs per
+// 16-byte read of a key, which the FMA pipes bound in long calls; short ones are bound by their two launches.  Products and
+// sums in fp32 throughout.  3 sequences of 16 heads, d = 128, over 1,000 entries: 11.0 us (split 5.8, join 5.1); the
+// weights of 500 slots 4.5 us.
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
