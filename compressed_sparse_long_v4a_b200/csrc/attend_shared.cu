@@ -15,8 +15,8 @@
 // memory (fp32 by asynchronous copies, all of a tile in flight).  For the scores a lane is a key; for the output it is a
 // slice of d, and each probability is broadcast from the lane that has it.  4 rows per warp mean 16 FMAs per
 // 16-byte read of a key, which the FMA pipes bound in long calls; short ones are bound by their two launches.  Products and
-// sums in fp32 throughout.  3 sequences of 16 heads, d = 128, over 1,000 entries: 11.0 us (split 5.8, join 5.1); the
-// weights of 500 slots 4.5 us.
+// sums in fp32 throughout.  3 sequences of 16 heads, d = 128, over 1,000 entries: 9.2 us (split 5.9, join 3.6, or 5.1 if
+// no piece's output is loaded before the weights are known); the weights of 500 slots 4.5 us.
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
@@ -260,6 +260,15 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_cons
     const long long row_own = ((long long)p.groups * p.splits + (query * p.head_tiles + h / kRowsB) * p.own_splits) * kRowsB + h % kRowsB;
     auto piece_row = [&](int i) -> long long { return i < n_pre ? row_pre + (long long)i * kRowsB : row_own + (long long)(i - n_pre) * kRowsB; };
     if (threadIdx.x == 0 && h == 0 && query % a.n_q == 0) report_sequence(a, b);
+    // the first pieces' outputs are on their way while the weights are worked out
+    constexpr int kAhead = 10;  // of each warp, in registers
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = warp + k * (kThreads / 32);
+        ahead[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n && lane * 4 < d) ahead[k] = __ldcg(reinterpret_cast<const float4*>(part_o + piece_row(i) * d + lane * 4));
+    }
     float m = -INFINITY;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const float x = part_ml[piece_row(i)].x;
@@ -287,8 +296,21 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_cons
     if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2F : (l == 0.f ? -INFINITY : l);
     for (int e = lane * 4; e < d; e += 128) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        int from = warp;
+        if (e == lane * 4) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = warp + k * (kThreads / 32);
+                const float wi = i < n ? w[i] : 0.f;
+                o.x = fmaf(wi, ahead[k].x, o.x);
+                o.y = fmaf(wi, ahead[k].y, o.y);
+                o.z = fmaf(wi, ahead[k].z, o.z);
+                o.w = fmaf(wi, ahead[k].w, o.w);
+            }
+            from += kAhead * (kThreads / 32);
+        }
 #pragma unroll 4
-        for (int i = warp; i < n; i += kThreads / 32) {
+        for (int i = from; i < n; i += kThreads / 32) {
             const float wi = w[i];
             const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + piece_row(i) * d + e));
             o.x = fmaf(wi, v.x, o.x);
