@@ -15,7 +15,7 @@
 // memory (fp32 by asynchronous copies, all of a tile in flight).  For the scores a lane is a key; for the output it is a
 // slice of d, and each probability is broadcast from the lane that has it.  4 rows per warp mean 16 FMAs per
 // 16-byte read of a key, which the FMA pipes bound in long calls; short ones are bound by their two launches.  Products and
-// sums in fp32 throughout.  3 sequences of 16 heads, d = 128, over 1,000 entries: 9.2 us (split 5.9, join 3.6, or 5.1 if
+// sums in fp32 throughout.  3 sequences of 16 heads, d = 128, over 1,000 entries: 9.3 us (split 5.9, join 3.6, or 5.1 if
 // no piece's output is loaded before the weights are known); the weights of 500 slots 4.5 us.
 #include "common.cuh"
 #include "internal.h"
@@ -243,8 +243,11 @@ __device__ __forceinline__ float block_reduce(float x, float* red, bool max) {
 
 __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ SimtPlan p,
                                                                const __grid_constant__ Turns turns, const float2* part_ml, const float* part_o) {
+    const bool f32 = a.out_dtype == V4A_F32;
     griddep_wait();
-    griddep_launch_dependents();
+    // bf16 rows may be the first query of an attention kernel, which reads it before it waits for this grid: it is let
+    // in when they have reached L2
+    if (f32) griddep_launch_dependents();
     __shared__ float w[kMaxPieces];  // weight of every piece
     __shared__ __align__(16) float sum[kThreads / 32][512];
     __shared__ float red[kThreads / 32];
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const __grid_cons
             *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + row * d + e) = __floats2bfloat162_rn(x, y);
         }
     }
+    if (!f32) __threadfence();
 }
 
 // Weights, fp32: a block takes 32 own slots of one sequence and runs over the sequence's rows (query, head), 32 at

@@ -29,7 +29,7 @@
 // ~3,200 cycles, 105 of the 128 bytes a cycle, and 96 KB into it from L2, 30 of the 45 bytes a cycle that loads
 // alone reach; the tensor cores are busy 2,100 of those cycles.  Tiles of 64 keys in four stages took 2,300
 // cycles per 64 keys and of 96 in three 1,750, against 1,610.  A piece costs another ~6,000 cycles (128 KB of O per CTA at
-// 32 bytes a cycle).  32 sequences of 64 heads over 8,192 shared entries: 49 us (43 + 8 for the join), 0.71 PFLOP/s, 43% of
+// 32 bytes a cycle).  32 sequences of 64 heads over 8,192 shared entries: 51 us (42 + 9 for the join), 0.68 PFLOP/s, 42% of
 // the measured bf16 peak.
 //
 // Masked places may hold anything.  A NaN or infinity in a row of K = V makes the raw S of every row of the
@@ -752,8 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 // Joins the pieces.  A block takes 32 rows (a lane each) and 16 dims (4 per warp): a warp's load of a
 // piece is 512 contiguous bytes.  The output leaves through shared memory, 32 or 64 bytes per row.
 __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_constant__ PairArgs c, const __grid_constant__ Turns turns) {
+    const bool f32 = c.a.out_dtype == V4A_F32;
     griddep_wait();
-    griddep_launch_dependents();
+    // The attention kernels read their first query before they wait for the grid before them; bf16 rows may be it, so the
+    // next kernel is let in when they have reached L2 (0.8 to 2 us a call more than letting it in here)
+    if (f32) griddep_launch_dependents();
     __shared__ float tile[32][20];
     const SharedArgs& a = c.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -863,6 +866,7 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
     } else {
         const __nv_bfloat162 p[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = *reinterpret_cast<const uint2*>(p);
+        __threadfence();
     }
 }
 

@@ -128,6 +128,34 @@ def test_workspace_of_the_call_on_another_stream(v4a):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("d,H", [(512, 64), (512, 8), (256, 128)])
+def test_output_as_the_next_calls_query(v4a, d, H):
+    # the attention kernels request their first query early: it must be the output of the call before, call after call
+    g = gen(49)
+    T = 512 // d * 64 // H if d * H < 32768 else 1  # [2][1][64][512] in all
+    prefix, ent = normal(g, (300, d), BF16).cuda(), normal(g, (2, 700, 512), BF16).cuda()
+    ring = torch.zeros((2, 1, 512), dtype=BF16, device="cuda")
+    qs = [normal(g, (2, T, H, d), BF16).cuda() for _ in range(6)]
+    mid, want, got = torch.empty_like(qs[0]), [], []
+
+    def step(q, wait):
+        v4a.v4a_hca_attend_shared(q, prefix, None, None, mid, m=128, window=0, ctx_len=128 * 300 + T)
+        if wait:
+            torch.cuda.synchronize()
+        o = torch.empty((2, 1, 64, 512), device="cuda")
+        v4a.v4a_hca_attend(mid.view(2, 1, 64, 512), ent, ring, 700 * 128 - 1, o, m=128, window=0, ctx_len=700 * 128)
+        return o
+
+    for q in qs:
+        want.append(step(q, True))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        got = [step(q, False) for q in qs]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ weights
 
 @pytest.mark.parametrize("dtype,H,d", [(F32, 3, 64), (BF16, 3, 64), (BF16, 20, 512)])
