@@ -327,6 +327,9 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         if (in_place && (r.x_batch_stride != r.out_batch_stride || r.x_tok_stride != r.out_tok_stride ||
                          r.x_head_stride != r.out_head_stride))
             return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: in place needs equal strides", i);
+        for (int j = 0; j < i; ++j)  // what their first elements show; streams may lie between each other's rows
+            if (r.out == io[j].out || r.out == io[j].x || r.x == io[j].out)
+                return report(V4A_ERR_INVALID_ARG, "v4a_rope: streams %d and %d overlap", j, i);
         RopeStream& s = a.s[i];
         s.x = r.x;
         s.out = r.out;

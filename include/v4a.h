@@ -447,7 +447,8 @@ typedef struct v4a_rope_params {
  * (v4a_attend_ext) is inverse = 1, half = 0 on the last R dims.
  * Errors: V4A_ERR_INVALID_ARG for NULL pointers, n_streams outside 0..8,
  * sizes or strides out of range, rows of out that overlap, x = out with
- * other strides; V4A_ERR_UNSUPPORTED for another dtype. */
+ * other strides, an out that begins where another stream's x or out does;
+ * V4A_ERR_UNSUPPORTED for another dtype. */
 V4A_API v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, long long n_tok,
                             const int64_t* positions, long long pos_stride, long long pos0, long long pos_step,
                             const v4a_rope_params* params, void* stream);

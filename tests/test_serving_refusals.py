@@ -66,6 +66,17 @@ def test_rope_streams_share_a_dtype(v4a):
     assert v4a.lib.v4a_rope(arr, 1, 2, 4, None, 0, 0, 1, None, None) == INVALID
 
 
+def test_rope_streams_that_write_over_each_other(v4a):
+    # the same tensor twice would be turned twice, or half of it, as the blocks happen to run
+    p = v4a.RopeParams(64, 0, 0, 10000.0, 1.0, 0, 32.0, 1.0, 1.0)
+    far, call = 64 * FAKE, lambda *ios: v4a.lib.v4a_rope((v4a.RopeIO * len(ios))(*ios), len(ios), 2, 4, None, 0, 0, 1, ctypes.byref(p), None)
+    one = rope_io(v4a)
+    for x, out in ((one.x, one.out), (far, one.out), (one.out, far), (far, one.x)):
+        assert call(one, rope_io(v4a, x=x, out=out)) == INVALID
+        assert call(one, rope_io(v4a, x=3 * far, out=4 * far), rope_io(v4a, x=x, out=out)) == INVALID
+    assert b"overlap" in v4a.lib.v4a_last_error()
+
+
 def cache(v, **kw):
     f = dict(prefix=FAKE, n_prefix=8, own=FAKE, own_rows=16, own_count=FAKE, own_entry=None, ring=FAKE, ring_rows=256,
              ctx_lens=FAKE)
