@@ -292,8 +292,8 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         return report(V4A_ERR_INVALID_ARG, "v4a_rope: rope_dims must be even and in 2..512");
     if (!(p.base > 0) || !(p.factor > 0) || !isfinite(p.base) || !isfinite(p.factor) || !isfinite(p.out_scale))
         return report(V4A_ERR_INVALID_ARG, "v4a_rope: base and factor must be > 0, out_scale finite");
-    if (p.orig_ctx < 0 || (p.orig_ctx > 0 && !(p.beta_fast > p.beta_slow)))
-        return report(V4A_ERR_INVALID_ARG, "v4a_rope: need orig_ctx >= 0 and, with it, beta_fast > beta_slow");
+    if (p.orig_ctx < 0 || (p.orig_ctx > 0 && !(p.beta_fast > p.beta_slow && isfinite(p.beta_fast) && isfinite(p.beta_slow))))
+        return report(V4A_ERR_INVALID_ARG, "v4a_rope: need orig_ctx >= 0 and, with it, finite beta_fast > beta_slow");
     if (n_streams == 0 || batch == 0 || n_tok == 0) return V4A_OK;
     if (!io) return report(V4A_ERR_INVALID_ARG, "v4a_rope: io is NULL");
     if (n_tok > 0x7fffffffLL || (long long)batch * n_tok > 0x7fffffffLL)

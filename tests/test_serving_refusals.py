@@ -66,6 +66,13 @@ def test_rope_streams_share_a_dtype(v4a):
     assert v4a.lib.v4a_rope(arr, 1, 2, 4, None, 0, 0, 1, None, None) == INVALID
 
 
+@pytest.mark.parametrize("kw", [dict(beta_fast=float("inf")), dict(beta_slow=float("-inf")), dict(beta_slow=float("nan"))])
+def test_rope_blend_without_bounds(v4a, kw):
+    # the blend would be 0 * inf: every angle a NaN
+    assert rope(v4a, orig_ctx=4096, n_tok=4, **kw) == INVALID
+    assert rope(v4a, orig_ctx=0, n_tok=0, **kw) == OK  # not used
+
+
 def test_rope_streams_that_write_over_each_other(v4a):
     # the same tensor twice would be turned twice, or half of it, as the blocks happen to run
     p = v4a.RopeParams(64, 0, 0, 10000.0, 1.0, 0, 32.0, 1.0, 1.0)
