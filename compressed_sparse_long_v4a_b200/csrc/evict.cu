@@ -352,6 +352,8 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     if (io->own_rows < 0 || io->d < 1 || io->d > 65536 || (io->d * es) % 16 || io->out_rows < budget)
         return report(V4A_ERR_INVALID_ARG, "v4a_evict: own_rows, d (rows in multiples of 16 bytes) or out_rows < budget");
     if (dev_status && reinterpret_cast<uintptr_t>(dev_status) % 4) return report(V4A_ERR_INVALID_ARG, "v4a_evict: dev_status misaligned");
+    if (io->entry_out && !io->own_entry && (long long)io->first_entry + io->own_rows - 1 > 0x7fffffffLL)
+        return report(V4A_ERR_INVALID_ARG, "v4a_evict: first_entry + own_rows passes 2^31");
     if (batch == 0) return V4A_OK;
     if ((io->own_rows > 0 && (!io->own || !io->weights)) || !io->own_out || !io->weights_out || !io->kept || !io->count_out)
         return report(V4A_ERR_INVALID_ARG, "v4a_evict: own, weights, own_out, weights_out, kept and count_out are required");
@@ -426,7 +428,7 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     };
     if (!launch(cs)) launch(8);
     if (e == cudaSuccess && io->own_rows > 0)
-        e = launch_pdl(evict_rows_kernel, dim3((unsigned)((budget + 31) / 32), (unsigned)batch), dim3(256), 0, st,
+        e = launch_pdl(evict_rows_kernel, dim3(((unsigned)budget + 31u) / 32u, (unsigned)batch), dim3(256), 0, st,
                        static_cast<const uint4*>(io->own), static_cast<uint4*>(io->own_out), (const int32_t*)io->kept,
                        io->own_rows, io->out_rows, budget, (int)(row / 16));
     if (e == cudaSuccess) e = cudaGetLastError();

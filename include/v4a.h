@@ -537,7 +537,8 @@ typedef struct v4a_evict_io {
  * left as they were.  Inputs and outputs may not overlap.
  * dev_status (nullable): V4A_ERR_DEVICE_FAULT for a count outside
  * 0 .. own_rows (clamped).  Errors: V4A_ERR_INVALID_ARG for NULL or misaligned
- * pointers, budget < 1, keep_first + keep_recent > budget, overlap. */
+ * pointers, budget < 1, keep_first + keep_recent > budget, overlap, entry
+ * numbers first_entry + slot that pass 2^31 - 1. */
 V4A_API v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, int keep_first, int keep_recent,
                              int* dev_status, void* stream);
 

@@ -163,6 +163,14 @@ def test_evict(v4a, kw, status):
     assert evict(v4a, **kw) == status
 
 
+def test_evict_entry_numbers_that_do_not_fit(v4a):
+    last = (1 << 31) - 32
+    assert evict(v4a, first_entry=last + 1) == INVALID and b"first_entry" in v4a.lib.v4a_last_error()
+    assert evict(v4a, first_entry=last, kept=None) == INVALID and b"first_entry" not in v4a.lib.v4a_last_error()  # 32 rows: they fit
+    for kw in (dict(own_entry=8 * FAKE), dict(entry_out=None)):  # not used
+        assert evict(v4a, first_entry=last + 1, kept=None, **kw) == INVALID and b"first_entry" not in v4a.lib.v4a_last_error()
+
+
 def test_null_structs(v4a):
     L = v4a.lib
     s = shape(v4a)
