@@ -610,6 +610,10 @@ v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, cons
         return report(V4A_ERR_INVALID_ARG, "%s: lse, weights_out and (with decay > 0) weights_in are required", what);
     if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4))
         return report(V4A_ERR_INVALID_ARG, "%s: lse or weights misaligned", what);
+    const uintptr_t w_in = reinterpret_cast<uintptr_t>(weights_in), w_out = reinterpret_cast<uintptr_t>(weights_out);
+    const uintptr_t w_bytes = (uintptr_t)a.batch * a.own_rows * 4;
+    if (decay != 0.f && w_in != w_out && w_in < w_out + w_bytes && w_out < w_in + w_bytes)
+        return report(V4A_ERR_INVALID_ARG, "%s: weights_in and weights_out overlap without being the same", what);
     a.lse = const_cast<float*>(lse);  // read only
     a.weights_in = weights_in;
     a.weights_out = weights_out;

@@ -505,7 +505,7 @@ V4A_API size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_pre
  * the slot's entry; a head with lse = -inf (no candidates) adds nothing.  With
  * the lse of v4a_hca_attend_shared the added terms are that call's softmax
  * weights.  weights_in / weights_out: [batch][own_rows] fp32, may be the
- * same; with decay = 0 weights_in is not read and may be NULL.  Slots beyond
+ * same, but not overlap in part; with decay = 0 weights_in is not read and may be NULL.  Slots beyond
  * the count are left as they were.  The sum's order is fixed: equal inputs give
  * equal bits.  The cache's prefix and ring are not read (n_prefix, lengths,
  * counts and entries are).  dev_status as v4a_hca_attend_shared. */

@@ -144,6 +144,14 @@ def test_attend_weights(v4a, kw, status):
                                       ctypes.byref(s), None) == status
 
 
+@pytest.mark.parametrize("by", [4, -4, 2 * 16 * 4 - 4, 4 - 2 * 16 * 4])
+def test_attend_weights_that_overlap_in_part(v4a, by):
+    # [2][16] weights, written while another block still reads them
+    c, s = cache(v4a), shape(v4a)
+    assert v4a.lib.v4a_attend_weights(FAKE, ctypes.byref(c), FAKE, 9 * FAKE, 9 * FAKE + by, 1.0, 1, None, ctypes.byref(s), None) == INVALID
+    assert b"overlap" in v4a.lib.v4a_last_error()
+
+
 def evict(v, batch=2, budget=8, first=1, recent=2, status=None, **kw):
     f = dict(own=FAKE, weights=2 * FAKE, own_count=None, own_entry=None, own_rows=32, d=64, dtype=1, own_out=3 * FAKE,
              weights_out=4 * FAKE, entry_out=5 * FAKE, kept=6 * FAKE, count_out=7 * FAKE, out_rows=8, first_entry=0)
