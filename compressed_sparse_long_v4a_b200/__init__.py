@@ -584,7 +584,8 @@ def v4a_hca_attend_shared(q, prefix, own, ring, out, *, m: int, window: int, ctx
     [batch][own_rows][d] (the first own_count[b] slots, holding entries own_entry[b]) and the window in ring
     [batch][ring_rows][d]; sequences are ctx_lens[b] tokens long (int64; None: ctx_len).  prefix, own and ring
     may be None.  out: float32, or bfloat16 with bfloat16 inputs; lse (float32 [batch][n_q][heads], optional)
-    receives the log of the softmax denominator."""
+    receives the log of the softmax denominator.  Without a workspace one is allocated (not while `stream`, other
+    than the current one, is being captured)."""
     _check(_binding.hca_attend_shared(q, prefix, own, ring, out, m, window, ctx_len, ctx_lens, own_count, own_entry,
                                       lse, workspace, dev_status, sink, rope_dims, rope_base, stream))
 

@@ -133,6 +133,15 @@ struct Place {
     }
 };
 
+bool capturing(void* stream) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &s) != cudaSuccess) {
+        (void)cudaGetLastError();  // the default stream while another one is captured: the call itself will say so
+        return false;
+    }
+    return s != cudaStreamCaptureStatusNone;
+}
+
 // wraps a function of (args, n): checks the count, turns C++ exceptions into Python's
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -277,6 +286,8 @@ PyObject* hca_attend_shared(PyObject*, PyObject* const* arg, Py_ssize_t n) {
         const Place at(dev, arg[17]);
         at::Tensor made;
         if (!workspace) {
+            if (at.other && capturing(at.stream))  // a graph would keep using memory that goes back to the allocator
+                throw ValueError("workspace is required where a stream that is not the current one is captured");
             const size_t bytes = v4a_shared_workspace_size(&sh, n_prefix, c.own_rows, dt);
             made = at::empty({(int64_t)std::max<size_t>(bytes, 256)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev.index));
             if (at.other)  // freed before the stream is through with it: the allocator has to know

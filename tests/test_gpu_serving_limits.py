@@ -128,6 +128,25 @@ def test_workspace_of_the_call_on_another_stream(v4a):
         torch.cuda.synchronize()
 
 
+def test_capture_on_another_stream_needs_a_workspace(v4a):
+    # the call's own workspace would go back to the allocator, and the graph would keep writing to it
+    q, prefix = torch.randn((2, 1, 4, 128), device="cuda"), torch.randn((50, 128), device="cuda")
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(v4a.v4a_shared_workspace_size(batch=2, heads=4, d=128, n_prefix=50, own_rows=0, dtype=F32), dtype=torch.uint8, device="cuda")
+    kw = dict(m=128, window=0, ctx_len=128 * 50)
+    v4a.v4a_hca_attend_shared(q, prefix, None, None, want, **kw)
+    torch.cuda.synchronize()
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            with pytest.raises(ValueError, match="workspace"):
+                v4a.v4a_hca_attend_shared(q, prefix, None, None, out, stream=side, **kw)
+            v4a.v4a_hca_attend_shared(q, prefix, None, None, out, workspace=ws, stream=side, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("d,H", [(512, 64), (512, 8), (256, 128)])
 def test_output_as_the_next_calls_query(v4a, d, H):
     # the attention kernels request their first query early: it must be the output of the call before, call after call
