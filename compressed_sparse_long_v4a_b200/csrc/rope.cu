@@ -3,11 +3,13 @@
 // Pair k of a row at position p turns by the angle p f_k, f_k = base^(-2k/R) (scaled for long contexts
 // on the host).  What is read and written once bounds it: 2 d elements per row (2 R in place), against
 // 3 flops per rotated element.  An item is 8 elements of a row (16 bytes of bf16).  A thread keeps one
-// column of items and runs down the heads of its token, so the column's angles stay in registers, the
+// column of items and runs down the heads of its token, so the column's angles stay in registers (of adjacent pairs), the
 // copied columns pass through as they are, and no index is worked out per item.  A block takes one
-// token, or several where their rows are few; its (cos, sin) are made once in shared memory while
-// the first rows are on their way.  Measured: 4,096 tokens of 64 x 512 bf16 89.6 us, 6.1 TB/s, 93% of the measured copy
-// bandwidth (an index per item and a barrier per token took 267 us); a decode step of four tokens 3.1 us on the
+// token, or several where their rows are few: its (cos, sin) are made once in shared memory while
+// the first rows are on their way, and that has to pay.  Then the rows of all its tokens are one run, and
+// the angles are read again for every row.  Measured: 4,096 tokens of 64 x 512 bf16 89.6 us, 6.1 TB/s, 93% of the measured copy
+// bandwidth (an index per item and a barrier per token took 267 us); 16,000 tokens of (8 + 1) x 512 and 4 x 128 65 us, 5.1 TB/s
+// (a token per block: 102 us), half pairs 69 us; 1,554 of 17 x 128 fp32, half pairs, 7.6 us; a decode step of four tokens 3.1 us on the
 // device.  With few tokens (a decode step) a token's heads are cut over blocks.
 #include "common.cuh"
 #include "internal.h"
@@ -18,14 +20,15 @@ namespace {
 
 constexpr int kMaxStreams = 8;
 constexpr int kThreads = 256;
-constexpr int kTable = kThreads;  // angles of a block's tokens at most: one per thread
+constexpr int kTable = 2 * kThreads;  // angles of a block's tokens at most
+constexpr int kMaxTok = 64;           // its tokens at most
 
 struct RopeStream {
     const void* x;
     void* out;
     int heads, off;
     int rot, row_items;  // items of a row: rotated ones first, then the copied ones
-    // vectors: tokens per block (1 unless a token's rows fit into it), heads side by side in it, and the blocks that a
+    // vectors: tokens per block (several where their rows are few), heads side by side in it, and the blocks that a
     // token's heads and columns are cut over; any alignment: blocks per token (h_parts)
     int tokens, h_par, h_parts, c_parts;
     unsigned block0;     // its first block
@@ -51,8 +54,7 @@ __device__ __forceinline__ X by_address(const X* p) {
 
 // (cos, sin) of n tokens from `tok` on: cs[i * pairs + k], one per thread
 __device__ __forceinline__ void make_table(const RopeArgs& a, unsigned tok, int n, float2* cs) {
-    const int i = threadIdx.x;
-    if (i < n * a.pairs) {
+    for (int i = threadIdx.x; i < n * a.pairs; i += kThreads) {
         const int k = i % a.pairs;
         const unsigned at = tok + i / a.pairs, b = at / (unsigned)a.n_tok, t = at % (unsigned)a.n_tok;
         const long long p = a.positions ? a.positions[b * a.pos_stride + t] : a.pos0 + t * a.pos_step;
@@ -112,11 +114,12 @@ __device__ __forceinline__ void rotate(Item<T>& u, Item<T>& v, const float2* w) 
 // Rows, offsets and strides in multiples of 8 elements: an item is one 8-element chunk, or, in the half
 // layout, the two chunks that a rotated item pairs up.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads, 4) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 5) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ __align__(16) float2 cs[kTable];
+    __shared__ long long from[2][kMaxTok];  // where the tokens begin in x and out
     griddep_wait();  // everything before this kernel on the stream has finished
     const RopeStream& s = which_stream(a);
-    constexpr int kU = sizeof(T) == 2 ? 4 : 2;  // rows in flight
+    constexpr int kU = sizeof(T) == 2 ? 2 : 1;  // rows in flight (twice as many with 4 blocks per SM: 4.2 instead of 4.7 TB/s)
     constexpr int kA = HALF ? 8 : 4;            // pairs of an item
     const int parts = s.h_parts * s.c_parts;
     const unsigned local = blockIdx.x - s.block0, group = local / (unsigned)parts;
@@ -137,40 +140,48 @@ __global__ void __launch_bounds__(kThreads, 4) rope_vec_kernel(const __grid_cons
         return c < s.rot ? e + s.off : e >= s.off ? e + 2 * a.pairs : e;
     };
     if (s.tokens > 1) {
-        // several tokens, a row of threads for each of their rows
-        const int per_tok = s.heads * s.row_items, items = n_tok * per_tok;
-        const T* xp[kU];
-        T* op[kU];
-        int at[kU];  // angles of a rotated item; -1: copied; -2: none
-        auto load = [&](int i0) {
+        // several tokens: this thread's column c, and its first row of (token, head)
+        if ((int)threadIdx.x < n_tok) {
+            const unsigned tok = tok0 + threadIdx.x, b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
+            from[0][threadIdx.x] = b * s.xb + t * s.xt;
+            from[1][threadIdx.x] = b * s.ob + t * s.ot;
+        }
+        __syncthreads();
+        const int r = (int)threadIdx.x / s.row_items, c = (int)threadIdx.x - r * s.row_items, rows = n_tok * s.heads;
+        const float per_head = 1.f / s.heads;
+        const bool rotated = c < s.rot;
+        const int e = element(c);
+        int row = r < s.h_par ? r : rows;
+        const T* const xp = static_cast<const T*>(s.x) + e;
+        T* const op = static_cast<T*>(s.out) + e;
+        auto token = [&](int at) { return (int)((at + 0.5f) * per_head); };  // exact: rows are few
+        auto load = [&]() {
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                const int i = i0 + j * kThreads;
-                at[j] = -2;
-                if (i >= items) continue;
-                const int i_tok = i / per_tok, r = i - i_tok * per_tok, h = r / s.row_items, c = r - h * s.row_items;
-                const unsigned tok = tok0 + i_tok, b = tok / (unsigned)a.n_tok, t = tok % (unsigned)a.n_tok;
-                const int e = element(c);
-                at[j] = c < s.rot ? i_tok * a.pairs + kA * c : -1;
-                xp[j] = static_cast<const T*>(s.x) + b * s.xb + t * s.xt + h * s.xh + e;
-                op[j] = static_cast<T*>(s.out) + b * s.ob + t * s.ot + h * s.oh + e;
-                u[j].load(xp[j]);
-                if (HALF && at[j] >= 0) v[j].load(xp[j] + a.pairs);
+                const int at = row + j * s.h_par, i = token(at);
+                if (at >= rows) continue;
+                const T* p = xp + (from[0][i] + (at - i * s.heads) * s.xh);
+                u[j].load(p);
+                if (HALF && rotated) v[j].load(p + a.pairs);
             }
         };
-        load(threadIdx.x);  // on its way while the angles are worked out
+        load();  // on its way while the angles are worked out
         make_table(a, tok0, n_tok, cs);
-        for (int i0 = threadIdx.x; i0 < items; i0 += kU * kThreads, load(i0)) {
+        while (row < rows) {
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                if (at[j] == -2) continue;
-                if (at[j] >= 0) {
-                    angles(at[j]);
+                const int at = row + j * s.h_par, i = token(at);
+                if (at >= rows) continue;
+                T* p = op + (from[1][i] + (at - i * s.heads) * s.oh);
+                if (rotated) {
+                    angles(i * a.pairs + kA * c);
                     rotate<T, HALF>(u[j], v[j], w);
-                    if (HALF) v[j].store(op[j] + a.pairs);
+                    if (HALF) v[j].store(p + a.pairs);
                 }
-                u[j].store(op[j]);
+                u[j].store(p);
             }
+            row += kU * s.h_par;
+            load();
         }
     } else {
         // one token: this thread's column c, and its first head
@@ -205,12 +216,13 @@ __global__ void __launch_bounds__(kThreads, 4) rope_vec_kernel(const __grid_cons
         };
         load();
         make_table(a, tok0, 1, cs);
-        if (on && rotated) angles(kA * c);
+        if (!HALF && on && rotated) angles(kA * c);
         while (h < s.heads) {
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
                 const int hj = h + j * step;
                 if (hj >= s.heads) continue;
+                if (HALF && rotated) angles(kA * c);  // 16 registers that spilled when held: 137 instead of 116 us
                 if (rotated) rotate<T, HALF>(u[j], v[j], w);
                 u[j].store(op + hj * s.oh);
                 if (HALF && rotated) v[j].store(op + hj * s.oh + a.pairs);
@@ -360,6 +372,9 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
     const long long tokens = (long long)batch * n_tok;
     a.all_tok = (unsigned)tokens;
     const long long want = (8LL * kNumSMs + tokens - 1) / tokens;  // blocks per token that fill the SMs
+    // items per thread that make a block worth its angles, and blocks per SM that are worth more than that (4 and 6:
+    // 16,000 tokens of half pairs 76 us where 8 and 4 take 69, 1,554 tokens of fp32 9.0 instead of 7.6 us, as 8 and 6 do)
+    constexpr int kWork = 8, kFill = 4;
     long long blocks = 0;
     for (int i = 0; i < n_streams; ++i) {
         RopeStream& s = a.s[i];
@@ -372,19 +387,18 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         } else if (s.row_items > kThreads) {
             s.c_parts = (s.row_items + kThreads - 1) / kThreads;
             most = s.heads;
-        } else if ((long long)s.heads * s.row_items <= kThreads && tokens > 1) {
-            // up to as many tokens as the table holds, while enough blocks remain to fill the SMs
-            s.h_par = s.heads;
-            s.tokens = kTable / a.pairs;
-            const long long even = (tokens + 2 * kNumSMs - 1) / (2 * kNumSMs);
-            const int room = kThreads / (s.heads * s.row_items);
-            if (s.tokens > even) s.tokens = (int)(even > room ? even : room < s.tokens ? room : s.tokens);
-            if (s.tokens > tokens) s.tokens = (int)tokens;
-            most = 1;
         } else {
+            const long long per_tok = (long long)s.heads * s.row_items;
+            // as many tokens as give each thread kWork items, while enough blocks remain to fill the SMs
+            long long most_tok = kWork * kThreads / per_tok, even = (tokens + kFill * kNumSMs - 1) / (kFill * kNumSMs), room = kThreads / per_tok;
+            if (most_tok > even) most_tok = even > room ? even : room;
+            if (most_tok > kTable / a.pairs) most_tok = kTable / a.pairs;
+            if (most_tok > kMaxTok) most_tok = kMaxTok;
+            if (most_tok > tokens) most_tok = tokens;
+            s.tokens = most_tok > 1 ? (int)most_tok : 1;
             s.h_par = kThreads / s.row_items;
-            if (s.h_par > s.heads) s.h_par = s.heads;
-            most = (s.heads + s.h_par - 1) / s.h_par;
+            if (s.h_par > s.heads * s.tokens) s.h_par = s.heads * s.tokens;
+            most = s.tokens > 1 ? 1 : (s.heads + s.h_par - 1) / s.h_par;
         }
         s.h_parts = (int)(want < most ? want : most);
         if (s.h_parts > 65535) s.h_parts = 65535;

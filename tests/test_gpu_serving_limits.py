@@ -261,3 +261,22 @@ def test_rope_tokens_of_few_rows(v4a, dtype, B, T, H, d, R, half, in_place):
     ref = su.rope_ref(x, pos, R, d - R, half)
     within(out, ref, su.rope_bound(x, ref, pos, R, d - R, rounding=su.BF if dtype == BF16 else su.U), "rope")
     assert torch.equal(out.cpu()[..., : d - R], x[..., : d - R])
+
+
+@pytest.mark.parametrize("dtype,B,T,H,d,R", [(BF16, 3, 333, 7, 512, 64), (F32, 2, 700, 31, 64, 32), (BF16, 1, 2500, 5, 256, 128), (BF16, 1, 12000, 1, 128, 32)])
+@pytest.mark.parametrize("half,in_place", [(False, False), (False, True), (True, False), (True, True)])
+def test_rope_blocks_of_several_tokens(v4a, dtype, B, T, H, d, R, half, in_place):
+    # enough tokens that a block takes several, with more rows than it has threads for; beside them one-head rows between
+    # others' rows, left as they were
+    g = gen(58)
+    x, kv = normal(g, (B, T, H, d), dtype), normal(g, (B, T, 3, d), dtype)
+    pos = torch.randint(0, 1 << 20, (B, T), generator=g)
+    dx, dkv = x.cuda(), kv.cuda()
+    out = dx if in_place else torch.full_like(dx, 7.0)
+    v4a.v4a_rope([(dx, out), (dkv[:, :, 1], dkv[:, :, 1])], rope_dims=R, positions=pos.cuda(), half=half, rope_offset=0)
+    rounding = su.BF if dtype == BF16 else su.U
+    for a, b in ((x, out), (kv[:, :, 1:2], dkv[:, :, 1:2])):
+        ref = su.rope_ref(a, pos, R, 0, half)
+        within(b, ref, su.rope_bound(a, ref, pos, R, 0, rounding=rounding), "rope")
+        assert torch.equal(b.cpu()[..., R:], a[..., R:])
+    assert torch.equal(dkv[:, :, ::2].cpu(), kv[:, :, ::2])
