@@ -20,7 +20,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
-#include "tc.cuh"
+#include "tc_pair.cuh"
 #include "turns.h"
 
 #include <type_traits>

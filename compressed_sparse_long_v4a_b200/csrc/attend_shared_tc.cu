@@ -46,7 +46,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
-#include "tc.cuh"
+#include "tc_pair.cuh"
 #include "turns.h"
 
 namespace v4a {

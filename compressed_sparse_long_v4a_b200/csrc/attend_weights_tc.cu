@@ -21,7 +21,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
-#include "tc.cuh"
+#include "tc_pair.cuh"
 
 namespace v4a {
 namespace {
