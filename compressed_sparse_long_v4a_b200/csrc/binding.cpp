@@ -8,7 +8,6 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -126,8 +125,9 @@ struct Place {
         if (given == Py_None) return;
         PyObject* p = PyObject_GetAttrString(given, "cuda_stream");
         if (!p) PyErr_Clear();
-        const long long v = integer(p ? p : given);
+        long long v = integer(p ? p : given);
         Py_XDECREF(p);
+        if (v == 1) v = 0;  // cudaStreamLegacy, the default stream, which torch knows as 0
         stream = reinterpret_cast<void*>(v);
         other = stream != current;
     }
@@ -289,11 +289,12 @@ PyObject* hca_attend_shared(PyObject*, PyObject* const* arg, Py_ssize_t n) {
             if (at.other && capturing(at.stream))  // a graph would keep using memory that goes back to the allocator
                 throw ValueError("workspace is required where a stream that is not the current one is captured");
             const size_t bytes = v4a_shared_workspace_size(&sh, n_prefix, c.own_rows, dt);
+            // From the pool of the stream that will use it: a block of another stream's may still be in use there, by
+            // kernels queued before its last owner let go of it, and goes back there while this stream uses it.
+            c10::cuda::OptionalCUDAStreamGuard used_on;
+            if (at.other)
+                used_on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(at.stream), (c10::DeviceIndex)dev.index));
             made = at::empty({(int64_t)std::max<size_t>(bytes, 256)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev.index));
-            if (at.other)  // freed before the stream is through with it: the allocator has to know
-                c10::cuda::CUDACachingAllocator::recordStream(
-                    made.storage().data_ptr(),
-                    c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(at.stream), (c10::DeviceIndex)dev.index));
             workspace = &made;
         }
         return v4a_hca_attend_shared(q->data_ptr(), &c, out->data_ptr(), out_dt, static_cast<float*>(ptr(lse)), dt, workspace->data_ptr(),

@@ -128,6 +128,31 @@ def test_workspace_of_the_call_on_another_stream(v4a):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_workspace_of_the_call_takes_no_memory_that_the_current_stream_still_uses(v4a, raw):
+    # a temporary of the current stream, let go of while kernels that read it are queued: its block may serve that stream
+    # again at once, but no other
+    c = shared_case(BF16, 16, 1, 64, 512, 4096, 70, 128, seed=59)
+    want, _ = attend(v4a, c)
+    dev = {k: c[k].cuda() for k in ("q", "prefix", "own", "ring")}
+    lens, cnt = torch.tensor(c["lens"]).cuda(), torch.tensor(c["counts"], dtype=torch.int32).cuda()
+    out = torch.empty_like(dev["q"])
+    size = v4a.v4a_shared_workspace_size(batch=16, heads=64, d=512, n_prefix=4096, own_rows=70, window=128)
+    copy = torch.empty(size, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        tmp = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(20_000_000)  # 10 ms: the call below is done long before
+        copy.copy_(tmp)
+        del tmp
+        v4a.v4a_hca_attend_shared(dev["q"], dev["prefix"], dev["own"], dev["ring"], out, m=128, window=128, ctx_len=c["ctx_len"],
+                                  ctx_lens=lens, own_count=cnt, stream=side.cuda_stream if raw else side)
+        side.synchronize()
+        assert torch.equal(out, want)
+        assert (copy == 7).all()
+
+
 def test_capture_on_another_stream_needs_a_workspace(v4a):
     # the call's own workspace would go back to the allocator, and the graph would keep writing to it
     q, prefix = torch.randn((2, 1, 4, 128), device="cuda"), torch.randn((50, 128), device="cuda")
