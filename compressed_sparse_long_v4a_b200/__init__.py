@@ -237,8 +237,19 @@ def v4a_version() -> int:
     return int(lib.v4a_version())
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """Scratch from the pool of the stream that will use it: a block of another stream's pool may still be in use
+    there, by kernels queued before its last owner let go of it."""
+    size = max(int(nbytes), 256)
+    raw = None if stream is None else _stream(stream)
+    if raw == 1:  # cudaStreamLegacy, the default stream, which torch knows as 0
+        raw = 0
+    if raw is None or raw == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)):
+        if torch.cuda.is_current_stream_capturing():  # a graph would keep using memory that goes back to the allocator
+            raise ValueError("workspace is required where a stream that is not the current one is captured")
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _io(x, gate, out, out_scale, out_exp=None) -> CompressIO:
@@ -331,7 +342,7 @@ def v4a_topk_mxfp4(q_i, w, k_codes, k_exp, idx_out, score_out=None, *, m: int, k
     B, T, HI, DI = q_i.shape
     s = _shape(batch=B, n_q=T, m=m, k=k, ctx_len=ctx_len)
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device, stream)
     _check(lib.v4a_topk_mxfp4(_ptr(q_i), _ptr(w), _ptr(k_codes), _ptr(k_exp), _ptr(idx_out), _ptr(score_out), HI, DI,
                               _dtype(q_i), _ptr(workspace), workspace.numel() * workspace.element_size(),
                               ctypes.byref(s), _stream(stream)))
@@ -354,7 +365,7 @@ def v4a_topk(q_i, w, k_i, k_scale, idx_out, score_out=None, *, m: int, k: int, c
     B, T, HI, DI = q_i.shape
     s = _shape(batch=B, n_q=T, m=m, k=k, ctx_len=ctx_len)
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device, stream)
     _check(lib.v4a_topk(_ptr(q_i), _ptr(w), _ptr(k_i), _ptr(k_scale), _ptr(idx_out), _ptr(score_out), HI, DI,
                         _dtype(q_i), _dtype(k_i), _ptr(workspace), workspace.numel() * workspace.element_size(),
                         ctypes.byref(s), _stream(stream)))
@@ -394,7 +405,7 @@ def v4a_csa_attend(q, entries, idx, token_kv, tok_pos0: int, out, *, m: int, win
     B, T, H, d = q.shape
     s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, k=idx.shape[-1], window=window, ctx_len=ctx_len)
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"csa_attend", ctypes.byref(s), 0, 0), q.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"csa_attend", ctypes.byref(s), 0, 0), q.device, stream)
     args = (_ptr(q), _ptr(entries), _ptr(idx), _ptr(token_kv), int(tok_pos0), int(token_kv.shape[1]), _ptr(out),
             _dtype(q), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status))
     ext = _ext(sink, rope_dims, rope_base)
@@ -412,7 +423,7 @@ def v4a_hca_attend(q, entries, token_kv, tok_pos0: int, out, *, m: int, window: 
     B, T, H, d = q.shape
     s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, window=window, ctx_len=ctx_len)
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"hca_attend", ctypes.byref(s), 0, 0), q.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"hca_attend", ctypes.byref(s), 0, 0), q.device, stream)
     args = (_ptr(q), _ptr(entries), _ptr(token_kv), int(tok_pos0), int(token_kv.shape[1]), _ptr(out), _dtype(q),
             _ptr(workspace), workspace.numel() * workspace.element_size())
     ext = _ext(sink, rope_dims, rope_base)
@@ -491,7 +502,7 @@ def v4a_topk_paged(q_i, w, k_pool, k_scale_pool, idx_out, score_out=None, *, m: 
     s = _shape(batch=B, n_q=T, m=m, k=k, ctx_len=ctx_len)
     pg = _paged(block_table, block_tokens, k_pool.shape[0] // (block_tokens // m))
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device, stream)
     _check(lib.v4a_topk_paged(_ptr(q_i), _ptr(w), _ptr(k_pool), _ptr(k_scale_pool), _ptr(idx_out), _ptr(score_out),
                               HI, DI, _dtype(q_i), _dtype(k_pool), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _ptr(dev_status), ctypes.byref(pg),
@@ -508,7 +519,7 @@ def v4a_topk_mxfp4_paged(q_i, w, k_codes_pool, k_exp_pool, idx_out, score_out=No
     s = _shape(batch=B, n_q=T, m=m, k=k, ctx_len=ctx_len)
     pg = _paged(block_table, block_tokens, k_codes_pool.shape[0] // (block_tokens // m))
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"topk", ctypes.byref(s), HI, DI), q_i.device, stream)
     _check(lib.v4a_topk_mxfp4_paged(_ptr(q_i), _ptr(w), _ptr(k_codes_pool), _ptr(k_exp_pool), _ptr(idx_out),
                                     _ptr(score_out), HI, DI, _dtype(q_i), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _ptr(dev_status), ctypes.byref(pg),
@@ -525,7 +536,7 @@ def v4a_csa_attend_paged(q, ent_pool, idx, ring, out, *, m: int, window: int, ct
     s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, k=idx.shape[-1], window=window, ctx_len=ctx_len)
     pg = _paged(block_table, block_tokens, ent_pool.shape[0] // (block_tokens // m), ring.shape[1])
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"csa_attend", ctypes.byref(s), 0, 0), q.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"csa_attend", ctypes.byref(s), 0, 0), q.device, stream)
     ext = _ext(sink, rope_dims, rope_base)
     _check(lib.v4a_csa_attend_paged(_ptr(q), _ptr(ent_pool), _ptr(idx), _ptr(ring), _ptr(out), _dtype(q),
                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
@@ -543,7 +554,7 @@ def v4a_hca_attend_paged(q, ent_pool, ring, out, *, m: int, window: int, ctx_len
     s = _shape(batch=B, n_q=T, heads=H, d=d, m=m, window=window, ctx_len=ctx_len)
     pg = _paged(block_table, block_tokens, ent_pool.shape[0] // (block_tokens // m), ring.shape[1])
     if workspace is None:
-        workspace = _workspace(lib.v4a_workspace_size(b"hca_attend", ctypes.byref(s), 0, 0), q.device)
+        workspace = _workspace(lib.v4a_workspace_size(b"hca_attend", ctypes.byref(s), 0, 0), q.device, stream)
     ext = _ext(sink, rope_dims, rope_base)
     _check(lib.v4a_hca_attend_paged(_ptr(q), _ptr(ent_pool), _ptr(ring), _ptr(out), _dtype(q), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _ptr(dev_status),
