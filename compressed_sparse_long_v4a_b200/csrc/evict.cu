@@ -41,6 +41,7 @@ struct EvictArgs {
 };
 
 constexpr int kList = 256;  // four threads rank each
+constexpr int kMaxStored = 44;  // keys per thread that stay in shared memory, 4 KB a block each
 
 struct __align__(16) EvictSmem {
     uint32_t hist[3][kBins];  // this block's counts, by pass
@@ -53,6 +54,7 @@ struct __align__(16) EvictSmem {
     uint32_t warp[32];
 };
 
+static_assert(sizeof(EvictSmem) + kMaxStored * kThreads * 4 <= 232448, "shared memory");
 static_assert(offsetof(EvictSmem, hist) % 8 == 0 && offsetof(EvictSmem, sums) % 8 == 0 && offsetof(EvictSmem, list) % 8 == 0 && offsetof(EvictSmem, last) % 8 == 0, "read in pairs");
 
 // Exclusive prefix sum of a number per warp (the same in all its lanes) over the block's warps; *sum: the block's total.  One
@@ -400,10 +402,11 @@ extern "C" v4a_status v4a_evict(const v4a_evict_io* io, int batch, int budget, i
     cudaError_t e = cudaSuccess;
     auto launch = [&](int blocks) {
         const long long per = ((long long)io->own_rows + blocks * kThreads - 1) / (blocks * kThreads);
-        const bool keep = per <= 44;  // 4 KB each
+        const bool keep = per <= kMaxStored;
         auto* kernel = keep ? evict_select_kernel<true> : evict_select_kernel<false>;
         const size_t smem = keep ? (size_t)per * kThreads * 4 : 0;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the most of any call: host threads share the attribute, and another one may set it before this launch
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, keep ? kMaxStored * kThreads * 4 : 0);
         if (e == cudaSuccess && blocks > 8) {
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             cudaLaunchConfig_t cfg = {};

@@ -1,0 +1,64 @@
+"""Two host threads calling the C ABI at once, each on a stream of its own, with sizes that ask for different amounts of
+shared memory of the same kernel: every call succeeds and gives what it gives alone."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+CALLS = 4000
+
+
+@pytest.fixture(scope="module")
+def v4a():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import compressed_sparse_long_v4a_b200 as v
+    return v
+
+
+def together(jobs):
+    """jobs: (call(stream) -> status, its outputs).  Runs each alone, then all of them at once, over and over."""
+    streams = [torch.cuda.Stream() for _ in jobs]
+    alone = []
+    for (call, outs), s in zip(jobs, streams):
+        assert call(s.cuda_stream) == 0
+        torch.cuda.synchronize()
+        alone.append([o.clone() for o in outs])
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    failed, start = [0] * len(jobs), threading.Barrier(len(jobs))
+
+    def run(i):
+        start.wait()
+        for _ in range(CALLS):
+            failed[i] += jobs[i][0](streams[i].cuda_stream) != 0
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(jobs)
+    for (_, outs), want in zip(jobs, alone):
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def evict_job(v4a, rows):
+    g = torch.Generator().manual_seed(rows)
+    own, w = torch.randn((1, rows, 8), generator=g).cuda(), torch.randn((1, rows), generator=g).cuda()
+    budget = rows // 2
+    outs = [torch.zeros((1, budget, 8), device="cuda"), torch.zeros((1, budget), device="cuda"),
+            torch.zeros((1, budget), dtype=torch.int32, device="cuda"), torch.zeros((1,), dtype=torch.int32, device="cuda")]
+    io = v4a.EvictIO(own.data_ptr(), w.data_ptr(), None, None, rows, 8, 0, outs[0].data_ptr(), outs[1].data_ptr(), None,
+                     outs[2].data_ptr(), outs[3].data_ptr(), budget, 0)
+    keep = (own, w, io)
+    return (lambda s, keep=keep: v4a.lib.v4a_evict(ctypes.byref(keep[2]), 1, budget, 1, 1, None, s)), outs
+
+
+def test_evict(v4a):
+    together([evict_job(v4a, 8192), evict_job(v4a, 1000)])
