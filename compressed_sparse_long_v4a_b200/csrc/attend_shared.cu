@@ -569,6 +569,7 @@ v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, v
     if (need > 0 && (!workspace || workspace_bytes < need))
         return report(V4A_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
     if (!aligned(workspace, 256)) return report(V4A_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (const cudaError_t e = bind_context(); e != cudaSuccess) return from_cuda(e, what);
     cudaStream_t s = (cudaStream_t)stream;
     if (dev_status) {
         const cudaError_t e = launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, s);
@@ -618,6 +619,7 @@ v4a_status v4a_attend_weights(const void* q, const v4a_shared_cache* cache, cons
     a.weights_in = weights_in;
     a.weights_out = weights_out;
     a.decay = decay;
+    if (const cudaError_t e = bind_context(); e != cudaSuccess) return from_cuda(e, what);
     cudaStream_t s = (cudaStream_t)stream;
     if (dev_status) {
         const cudaError_t e = launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, s);

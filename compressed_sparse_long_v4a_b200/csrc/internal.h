@@ -42,6 +42,9 @@ v4a_status report(v4a_status st, const char* fmt, ...);
 // Zero n 32-bit words with a kernel launched like every other kernel here, after the previous
 // work on the stream (a memset node in its place would end the chain of overlapped launches).
 cudaError_t launch_zero_words(uint32_t* p, long long n, cudaStream_t stream);
+// Encoding a tensor map is a driver call and needs a current context, which a host thread that has not called the
+// runtime yet does not have: every entry point that may encode one calls this first.
+cudaError_t bind_context();
 
 // ---- compress.cu ------------------------------------------------------
 cudaError_t launch_compress(const v4a_compress_io* kv, const v4a_compress_io* idx, int batch, long long n_tok,

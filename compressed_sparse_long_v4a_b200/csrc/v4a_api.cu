@@ -1,4 +1,5 @@
 // v4a_api.cu -- the exported C ABI: argument checks, then the launchers.
+#include <cudaTypedefs.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -28,6 +29,21 @@ cudaError_t launch_zero_words(uint32_t* p, long long n, cudaStream_t stream) {
     const cudaError_t e =
         launch_pdl(zero_words_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, stream, p, n);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t bind_context() {
+    static const auto current = []() -> PFN_cuCtxGetCurrent_v4000 {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p)
+                   : nullptr;
+    }();
+    CUcontext c = nullptr;
+    if (current && current(&c) == CUDA_SUCCESS && c) return cudaSuccess;
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    return e == cudaSuccess ? cudaSetDevice(device) : e;
 }
 
 }  // namespace v4a
@@ -228,6 +244,7 @@ static v4a_status topk_common(const v4a::IndexArgs& a, int32_t* idx_out, float* 
     if (!workspace || workspace_bytes < need)
         return fail(V4A_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
     if (!aligned(workspace, 256)) return fail(V4A_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (const cudaError_t e = v4a::bind_context(); e != cudaSuccess) return from_cuda(e, what);
     return from_cuda(v4a::launch_topk(a, shape->k, idx_out, score_out, workspace, workspace_bytes,
                                       (cudaStream_t)stream),
                      what);
@@ -278,6 +295,7 @@ v4a_status v4a_index_scores(const void* q_i, const float* w, const void* k_i, co
     v4a_status st = index_args(q_i, w, k_i, k_scale, nullptr, heads_i, d_i, q_dtype, k_dtype, shape, &a);
     if (st != V4A_OK) return st;
     if (!scores && a.n_ent > 0) return fail(V4A_ERR_INVALID_ARG, "scores is required");
+    if (const cudaError_t e = v4a::bind_context(); e != cudaSuccess) return from_cuda(e, "v4a_index_scores");
     return from_cuda(v4a::launch_index_scores(a, scores, (cudaStream_t)stream), "v4a_index_scores");
 }
 
@@ -288,6 +306,7 @@ v4a_status v4a_index_scores_mxfp4(const void* q_i, const float* w, const uint8_t
     v4a_status st = index_args(q_i, w, k_codes, nullptr, k_exp, heads_i, d_i, q_dtype, V4A_MXFP4, shape, &a);
     if (st != V4A_OK) return st;
     if (!scores && a.n_ent > 0) return fail(V4A_ERR_INVALID_ARG, "scores is required");
+    if (const cudaError_t e = v4a::bind_context(); e != cudaSuccess) return from_cuda(e, "v4a_index_scores_mxfp4");
     return from_cuda(v4a::launch_index_scores(a, scores, (cudaStream_t)stream), "v4a_index_scores_mxfp4");
 }
 
@@ -441,8 +460,9 @@ static v4a_status attend_common(const void* q, const void* entries, const int32_
         cudaError_t e = v4a::launch_zero_words(reinterpret_cast<uint32_t*>(dev_status), 1, (cudaStream_t)stream);
         if (e != cudaSuccess) return from_cuda(e, "dev_status reset");
     }
-    return from_cuda(v4a::launch_attend(a, workspace, workspace_bytes, (cudaStream_t)stream),
-                     csa ? "v4a_csa_attend" : "v4a_hca_attend");
+    const char* const call = csa ? "v4a_csa_attend" : "v4a_hca_attend";
+    if (const cudaError_t e = v4a::bind_context(); e != cudaSuccess) return from_cuda(e, call);
+    return from_cuda(v4a::launch_attend(a, workspace, workspace_bytes, (cudaStream_t)stream), call);
 }
 
 v4a_status v4a_csa_attend(const void* q, const void* entries, const int32_t* idx, const void* token_kv,
