@@ -351,7 +351,8 @@ cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t st) {
         !make_map(&q_map, a.q, 1, (long long)a.batch * c.per_seq, a.d, c.cols))
         return cudaErrorNotSupported;
     const long long items = (tiles + c.tiles - 1) / c.tiles;
-    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most of any call: host threads share the attribute, and another one may set it before this launch
+    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
     if (e == cudaSuccess)
         e = launch_pdl(weights_tc_kernel, dim3((unsigned)(items < kNumSMs ? items : kNumSMs)), dim3(kThreads), smem, st, own_map,
                        q_map, c);

@@ -18,7 +18,7 @@ def v4a():
     return v
 
 
-def together(jobs):
+def together(jobs, calls=CALLS):
     """jobs: (call(stream) -> status, its outputs).  Runs each alone, then all of them at once, over and over."""
     streams = [torch.cuda.Stream() for _ in jobs]
     alone = []
@@ -33,7 +33,7 @@ def together(jobs):
 
     def run(i):
         start.wait()
-        for _ in range(CALLS):
+        for _ in range(calls):
             failed[i] += jobs[i][0](streams[i].cuda_stream) != 0
 
     threads = [threading.Thread(target=run, args=(i,)) for i in range(len(jobs))]
@@ -62,3 +62,18 @@ def evict_job(v4a, rows):
 
 def test_evict(v4a):
     together([evict_job(v4a, 8192), evict_job(v4a, 1000)])
+
+
+def weights_job(v4a, heads):
+    g = torch.Generator().manual_seed(heads)
+    q, own = torch.randn((1, 1, heads, 512), generator=g).bfloat16().cuda(), torch.randn((1, 200, 512), generator=g).bfloat16().cuda()
+    lse, out = torch.full((1, 1, heads), 4.0, device="cuda"), torch.zeros((1, 200), device="cuda")
+    c = v4a.SharedCache(None, 0, own.data_ptr(), 200, None, None, None, 0, None)
+    s = v4a.Shape(1, 1, heads, 512, 128, 0, 0, 128 * 200)
+    keep = (q, own, lse, out, c, s)
+    return (lambda st, keep=keep: v4a.lib.v4a_attend_weights(keep[0].data_ptr(), ctypes.byref(keep[4]), keep[2].data_ptr(), None,
+                                                             keep[3].data_ptr(), 0.0, 1, None, ctypes.byref(keep[5]), st)), [out]
+
+
+def test_weights(v4a):
+    together([weights_job(v4a, 64), weights_job(v4a, 3), weights_job(v4a, 5)], 20000)
