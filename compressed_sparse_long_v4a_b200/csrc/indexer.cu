@@ -903,6 +903,10 @@ __global__ void __launch_bounds__(kFastThreads) topk_rows_kernel(const float* sc
     finish_lists(sc, k, n_def, n_cand, defs, cidx, ckey, sels, io, so);
 }
 
+// The most shared memory that any call asks for (heads_i * d_i <= 32,768, heads_i <= 64): host threads share the kernels'
+// limit, and another one may set it before this call launches.
+constexpr int kScoreMaxSmem = 4 * (32768 + 64);
+
 template <int HMAX>
 cudaError_t launch_scores_h(const IndexArgs& a, float* scores, cudaStream_t stream) {
     long long nblk = (a.n_ent + kScoreThreads - 1) / kScoreThreads;
@@ -911,29 +915,29 @@ cudaError_t launch_scores_h(const IndexArgs& a, float* scores, cudaStream_t stre
     switch (a.k_dtype) {
     case V4A_F32: {
         auto kern = index_score_kernel<HMAX, V4A_F32>;
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        const cudaError_t le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
+        cudaError_t le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreMaxSmem);
+        if (le == cudaSuccess) le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
         if (le != cudaSuccess) return le;
         break;
     }
     case V4A_BF16: {
         auto kern = index_score_kernel<HMAX, V4A_BF16>;
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        const cudaError_t le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
+        cudaError_t le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreMaxSmem);
+        if (le == cudaSuccess) le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
         if (le != cudaSuccess) return le;
         break;
     }
     case V4A_MXFP4: {
         auto kern = index_score_kernel<HMAX, V4A_MXFP4>;
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        const cudaError_t le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
+        cudaError_t le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreMaxSmem);
+        if (le == cudaSuccess) le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
         if (le != cudaSuccess) return le;
         break;
     }
     default: {
         auto kern = index_score_kernel<HMAX, V4A_FP8E4M3>;
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        const cudaError_t le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
+        cudaError_t le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreMaxSmem);
+        if (le == cudaSuccess) le = launch_pdl(kern, grid, dim3(kScoreThreads), smem, stream, a, scores);
         if (le != cudaSuccess) return le;
         break;
     }

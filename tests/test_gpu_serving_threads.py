@@ -77,3 +77,17 @@ def weights_job(v4a, heads):
 
 def test_weights(v4a):
     together([weights_job(v4a, 64), weights_job(v4a, 3), weights_job(v4a, 5)], 20000)
+
+
+def scores_job(v4a, heads, d):
+    g = torch.Generator().manual_seed(heads)
+    q, w = torch.randn((1, 1, heads, d), generator=g).cuda(), torch.rand((1, 1, heads), generator=g).cuda()
+    k, out = torch.randn((1, 64, d), generator=g).cuda(), torch.zeros((1, 1, 64), device="cuda")
+    s = v4a.Shape(1, 1, 0, 0, 4, 0, 0, 256)
+    keep = (q, w, k, out, s)
+    return (lambda st, keep=keep: v4a.lib.v4a_index_scores(keep[0].data_ptr(), keep[1].data_ptr(), keep[2].data_ptr(), None,
+                                                           keep[3].data_ptr(), heads, d, 0, 0, ctypes.byref(keep[4]), st)), [out]
+
+
+def test_index_scores(v4a):
+    together([scores_job(v4a, 64, 512), scores_job(v4a, 40, 8), scores_job(v4a, 36, 16)], 20000)
