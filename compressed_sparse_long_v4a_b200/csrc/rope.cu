@@ -289,6 +289,59 @@ bool rows_apart(long long d, long long n0, long long s0, long long n1, long long
     return true;
 }
 
+// What a stream's rows touch on one side: n[0] x n[1] x n[2] pieces of `bytes` from `at` on, s bytes apart.
+struct Extent {
+    uintptr_t at;
+    long long bytes, n[3], s[3];
+    long long reach() const { return (n[0] - 1) * s[0] + (n[1] - 1) * s[1] + (n[2] - 1) * s[2] + bytes; }
+};
+
+// Whether whole numbers v[i] in lo[i] .. hi[i], i >= k, make delta + sum v[i] s[i] lie in low .. high.  The strides
+// descend, and where each is at least what the smaller ones reach together, as in rows that lie apart, a level has three
+// values to try at most.  `budget` bounds the search for others: when it is used up, the answer is yes.
+bool meets(long long delta, long long low, long long high, const long long* s, const long long* lo, const long long* hi, int n, int k, int& budget) {
+    if (k == n) return low <= delta && delta <= high;
+    if (--budget < 0) return true;
+    long long least = 0, most = 0;  // of the smaller strides' sum
+    for (int i = k + 1; i < n; ++i) {
+        least += lo[i] * s[i];
+        most += hi[i] * s[i];
+    }
+    auto floor_div = [](long long a, long long b) { return a / b - (a % b < 0); };
+    long long v0 = -floor_div(-(low - delta - most), s[k]), v1 = floor_div(high - delta - least, s[k]);
+    v0 = v0 > lo[k] ? v0 : lo[k];
+    v1 = v1 < hi[k] ? v1 : hi[k];
+    for (long long v = v0; v <= v1; ++v)
+        if (meets(delta + v * s[k], low, high, s, lo, hi, n, k + 1, budget)) return true;
+    return false;
+}
+
+// whether two streams' rows share a byte; rows of one may lie between those of the other (heads of one projection)
+bool overlap(const Extent& a, const Extent& b) {
+    if (a.at + (uintptr_t)a.reach() <= b.at || b.at + (uintptr_t)b.reach() <= a.at) return false;
+    // row j of b begins at b.at - a.at + sum j s_b - sum i s_a behind row i of a; equal strides are one number j - i
+    long long s[6], lo[6], hi[6];
+    int n = 0;
+    auto add = [&](long long stride, long long from, long long to) {
+        if (stride == 0 || from == to) return;
+        int k = 0;
+        while (k < n && s[k] > stride) ++k;
+        if (k < n && s[k] == stride) {
+            lo[k] += from;
+            hi[k] += to;
+            return;
+        }
+        for (int i = n++; i > k; --i) s[i] = s[i - 1], lo[i] = lo[i - 1], hi[i] = hi[i - 1];
+        s[k] = stride, lo[k] = from, hi[k] = to;
+    };
+    for (int i = 0; i < 3; ++i) {
+        add(a.s[i], -(a.n[i] - 1), 0);
+        add(b.s[i], 0, b.n[i] - 1);
+    }
+    int budget = 10000;
+    return meets((long long)(b.at - a.at), 1 - b.bytes, a.bytes - 1, s, lo, hi, n, 0, budget);
+}
+
 }  // namespace
 }  // namespace v4a
 
@@ -314,6 +367,7 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         return report(V4A_ERR_INVALID_ARG, "v4a_rope: positions misaligned or pos_stride < 0");
 
     RopeArgs a;
+    Extent read[kMaxStreams], written[kMaxStreams];
     bool vec = true;
     for (int i = 0; i < n_streams; ++i) {
         v4a_rope_io r = io[i];
@@ -333,14 +387,28 @@ extern "C" v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, 
         if (r.x_batch_stride < 0 || r.x_tok_stride < 0 || r.x_head_stride < 0 || r.out_batch_stride < 0 ||
             r.out_tok_stride < 0 || r.out_head_stride < 0)
             return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: negative stride", i);
+        const long long counts[3] = {batch, n_tok, r.heads}, strides[2][3] = {{r.x_batch_stride, r.x_tok_stride, r.x_head_stride},
+                                                                               {r.out_batch_stride, r.out_tok_stride, r.out_head_stride}};
+        for (const auto& side : strides)
+            for (int k = 0; k < 3; ++k)
+                if (counts[k] > 1 && side[k] > (1LL << 48) / (counts[k] - 1))
+                    return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: stride out of range", i);
         if (!rows_apart(r.d, batch, r.out_batch_stride, n_tok, r.out_tok_stride, r.heads, r.out_head_stride))
             return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: rows of out overlap", i);
         const bool in_place = r.x == r.out;
         if (in_place && (r.x_batch_stride != r.out_batch_stride || r.x_tok_stride != r.out_tok_stride ||
                          r.x_head_stride != r.out_head_stride))
             return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: in place needs equal strides", i);
-        for (int j = 0; j < i; ++j)  // what their first elements show; streams may lie between each other's rows
-            if (r.out == io[j].out || r.out == io[j].x || r.x == io[j].out)
+        // what is read and written; in place that is the rotated dims alone
+        const long long first = in_place ? r.rope_offset * es : 0, touched = (in_place ? p.rope_dims : r.d) * es;
+        read[i] = {reinterpret_cast<uintptr_t>(r.x) + first, touched, {batch, n_tok, r.heads},
+                   {r.x_batch_stride * es, r.x_tok_stride * es, r.x_head_stride * es}};
+        written[i] = {reinterpret_cast<uintptr_t>(r.out) + first, touched, {batch, n_tok, r.heads},
+                      {r.out_batch_stride * es, r.out_tok_stride * es, r.out_head_stride * es}};
+        if (!in_place && overlap(read[i], written[i]))
+            return report(V4A_ERR_INVALID_ARG, "v4a_rope: stream %d: x and out overlap without being the same", i);
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i], written[j]) || overlap(written[i], read[j]) || overlap(read[i], written[j]))
                 return report(V4A_ERR_INVALID_ARG, "v4a_rope: streams %d and %d overlap", j, i);
         RopeStream& s = a.s[i];
         s.x = r.x;

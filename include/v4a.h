@@ -411,7 +411,8 @@ V4A_API v4a_status v4a_hca_attend_paged(const void* q, const void* entries, cons
 typedef struct v4a_rope_io {
     const void* x;                /* input rows */
     void* out;                    /* output rows; may be x itself with the same strides (in place: only the
-                                     rotated dims are touched); no other overlap with any x */
+                                     rotated dims are touched); no other overlap with any x or other out.  Rows of
+                                     one stream may lie between those of another */
     int heads;                    /* rows per token */
     int d;                        /* elements per row */
     int rope_offset;              /* the rotated dims are [rope_offset, rope_offset + rope_dims) */
@@ -447,8 +448,10 @@ typedef struct v4a_rope_params {
  * (v4a_attend_ext) is inverse = 1, half = 0 on the last R dims.
  * Errors: V4A_ERR_INVALID_ARG for NULL pointers, n_streams outside 0..8,
  * sizes or strides out of range, rows of out that overlap, x = out with
- * other strides, an out that begins where another stream's x or out does;
- * V4A_ERR_UNSUPPORTED for another dtype. */
+ * other strides, an out that shares a byte with an x (but in place) or
+ * another out (also where rows of different strides are interleaved so that
+ * 10,000 steps of a search do not tell them apart); V4A_ERR_UNSUPPORTED for
+ * another dtype. */
 V4A_API v4a_status v4a_rope(const v4a_rope_io* io, int n_streams, int batch, long long n_tok,
                             const int64_t* positions, long long pos_stride, long long pos0, long long pos_step,
                             const v4a_rope_params* params, void* stream);

@@ -305,3 +305,35 @@ def test_rope_blocks_of_several_tokens(v4a, dtype, B, T, H, d, R, half, in_place
         within(b, ref, su.rope_bound(a, ref, pos, R, 0, rounding=rounding), "rope")
         assert torch.equal(b.cpu()[..., R:], a[..., R:])
     assert torch.equal(dkv[:, :, ::2].cpu(), kv[:, :, ::2])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rope_streams_between_each_others_rows(v4a, dtype):
+    # one fused tensor: two parts of the same rows in place, heads in place, and heads written over others that nobody reads
+    g = gen(62)
+    fused = normal(g, (2, 5, 9, 256), dtype)
+    pos = torch.randint(0, 1 << 20, (2, 5), generator=g)
+    f = fused.cuda()
+    v4a.v4a_rope([(f[:, :, 0:2], f[:, :, 0:2]), (f[:, :, 0:2, :128], f[:, :, 0:2, :128]), (f[:, :, 2], f[:, :, 2]), (f[:, :, 3:6], f[:, :, 6:9])],
+                 rope_dims=64, positions=pos.cuda())
+    rounding = su.BF if dtype == BF16 else su.U
+
+    def check(got, x, off):
+        ref = su.rope_ref(x, pos, 64, off)
+        within(got[..., off : off + 64], ref[..., off : off + 64], su.rope_bound(x, ref, pos, 64, off, rounding=rounding)[..., off : off + 64], "rope")
+
+    check(f[:, :, 0:3], fused[:, :, 0:3], 192)
+    check(f[:, :, 0:2], fused[:, :, 0:2], 64)
+    check(f[:, :, 6:9], fused[:, :, 3:6], 192)
+    f = f.cpu()
+    assert torch.equal(f[:, :, 3:6], fused[:, :, 3:6]) and torch.equal(f[:, :, 6:9, :192], fused[:, :, 3:6, :192])
+    assert torch.equal(f[:, :, 0:2, :64], fused[:, :, 0:2, :64]) and torch.equal(f[:, :, 0:2, 128:192], fused[:, :, 0:2, 128:192])
+    assert torch.equal(f[:, :, 2, :192], fused[:, :, 2, :192])
+
+
+def test_rope_refuses_an_out_shifted_against_its_x(v4a):
+    x = torch.zeros((1, 9, 4, 64), device="cuda")
+    with pytest.raises(v4a.V4AError, match="overlap"):
+        v4a.v4a_rope([(x[:, :8], x[:, 1:])], rope_dims=64)
+    with pytest.raises(v4a.V4AError, match="overlap"):
+        v4a.v4a_rope([(x[:, :4], x[:, 4:8]), (x[:, 5:9], x[:, 5:9])], rope_dims=64)

@@ -84,6 +84,89 @@ def test_rope_streams_that_write_over_each_other(v4a):
     assert b"overlap" in v4a.lib.v4a_last_error()
 
 
+# The overlap checks of v4a_rope.  A last stream of another dtype is refused for that (UNSUPPORTED) once all others have
+# been accepted, so nothing is ever launched.
+def rope_overlap(v4a, ios, batch, n_tok, rope_dims):
+    p = v4a.RopeParams(rope_dims, 0, 0, 10000.0, 1.0, 0, 32.0, 1.0, 1.0)
+    arr = (v4a.RopeIO * (len(ios) + 1))(*ios, rope_io(v4a, dtype=3))
+    status = v4a.lib.v4a_rope(arr, len(ios) + 1, batch, n_tok, None, 0, 0, 1, ctypes.byref(p), None)
+    if status == UNSUPPORTED:
+        return False
+    assert status == INVALID and b"overlap" in v4a.lib.v4a_last_error() and b"rows of out" not in v4a.lib.v4a_last_error()
+    return True
+
+
+@pytest.mark.parametrize("shift", [2, 64, 128, 512, 1024, 2 * (1024 + 256) - 2])
+@pytest.mark.parametrize("back", [False, True])
+def test_rope_out_that_overlaps_its_own_x_in_part(v4a, shift, back):
+    # [2][4][4][64] bf16 with rows of one token 512 bytes, of one sequence 2,048 bytes apart: by elements, rows, tokens
+    io = rope_io(v4a, x=8 * FAKE, out=8 * FAKE + (-shift if back else shift))
+    assert rope_overlap(v4a, [io], 2, 4, 64)
+
+
+def test_rope_rows_between_those_of_others(v4a):
+    # heads of one fused projection [2][4][9][64]: in place, and from one part of it to another
+    s = dict(x_batch_stride=4 * 576, x_tok_stride=576, x_head_stride=64, out_batch_stride=4 * 576, out_tok_stride=576, out_head_stride=64)
+    at = lambda h: FAKE + 128 * h
+    heads = lambda x, out, n: rope_io(v4a, x=at(x), out=at(out), heads=n, **s)
+    assert not rope_overlap(v4a, [heads(0, 0, 4), heads(4, 4, 4), heads(8, 8, 1)], 2, 4, 64)
+    assert not rope_overlap(v4a, [heads(0, 4, 4), heads(8, 8, 1)], 2, 4, 64)
+    assert rope_overlap(v4a, [heads(0, 4, 5)], 2, 4, 64)  # its last head is the first of the outputs
+    assert rope_overlap(v4a, [heads(0, 0, 4), heads(3, 3, 4)], 2, 4, 64)
+    assert rope_overlap(v4a, [heads(0, 0, 4), heads(8, 4, 1), heads(4, 4, 1)], 2, 4, 64)
+    # in place, two parts of the same rows: only the rotated dims count
+    part = lambda off: rope_io(v4a, x=FAKE, out=FAKE, rope_offset=off)
+    assert not rope_overlap(v4a, [part(0), part(32)], 2, 4, 32)
+    assert rope_overlap(v4a, [part(0), part(30)], 2, 4, 32)
+
+
+def test_rope_overlap_agrees_with_counting(v4a):
+    import itertools
+    import random
+    rng = random.Random(1)
+    seen = [0, 0]
+
+    def layout(n, d):  # strides (batch, token, head) in elements that keep rows apart
+        order, reach, s = rng.sample(range(3), 3), d, [0, 0, 0]
+        for k in order:
+            s[k] = reach + rng.choice([0, 0, 1, d, 3 * d])
+            reach += (n[k] - 1) * s[k]
+        return s
+
+    for _ in range(4000):
+        B, T, R = rng.randint(1, 3), rng.randint(1, 4), 2 * rng.randint(1, 2)
+        ios, touched = [], []
+        common = None
+        for _ in range(rng.randint(1, 2)):
+            H, d = rng.randint(1, 3), R + rng.randint(0, 3)
+            xs = layout((B, T, H), d)
+            if common and rng.random() < 0.5:
+                xs, H, d = common
+            common = (xs, H, d)
+            x = FAKE + 2 * rng.randint(0, 120)
+            in_place = rng.random() < 0.5
+            os_ = xs if in_place or rng.random() < 0.5 else layout((B, T, H), d)
+            out, off = x if in_place else FAKE + 2 * rng.randint(0, 240), rng.randint(0, d - R)
+            if not in_place and out == x:
+                continue
+            ios.append(rope_io(v4a, x=x, out=out, heads=H, d=d, rope_offset=off, x_batch_stride=xs[0], x_tok_stride=xs[1], x_head_stride=xs[2],
+                               out_batch_stride=os_[0], out_tok_stride=os_[1], out_head_stride=os_[2]))
+            dims = range(off, off + R) if in_place else range(d)
+            cells = lambda at, s: {at // 2 + b * s[0] + t * s[1] + h * s[2] + e for b, t, h, e in itertools.product(range(B), range(T), range(H), dims)}
+            touched.append((cells(x, xs), cells(out, os_), in_place))
+        bad = any(not p and r & w for r, w, p in touched)
+        for (r0, w0, _), (r1, w1, _) in itertools.combinations(touched, 2):
+            bad = bad or bool(w0 & w1 or w0 & r1 or r0 & w1)
+        assert rope_overlap(v4a, ios, B, T, R) == bad
+        seen[bad] += 1
+    assert min(seen) > 500
+
+
+def test_rope_strides_that_pass_every_address(v4a):
+    assert rope(v4a, rope_io(v4a, x_tok_stride=1 << 61)) == INVALID
+    assert rope(v4a, rope_io(v4a, out_batch_stride=1 << 62)) == INVALID
+
+
 def cache(v, **kw):
     f = dict(prefix=FAKE, n_prefix=8, own=FAKE, own_rows=16, own_count=FAKE, own_entry=None, ring=FAKE, ring_rows=256,
              ctx_lens=FAKE)
