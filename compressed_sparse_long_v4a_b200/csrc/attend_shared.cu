@@ -352,7 +352,7 @@ template <int D>
 struct __align__(16) WeightTile {
     float k[kKeys][D + 4];
     float q[kWRows][D];
-    float lse[kWRows];      // times log2 e; -inf: no candidates, or no such row
+    float lse[kWRows];      // -inf: no candidates, or no such row
     long long seen[kWRows];
     float sums[kWThreads / 32][kKeys];
 };
@@ -381,14 +381,14 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(SharedArgs a) {
         if (warp == 0 && a.decay != 0.f) before = a.weights_in[at];
     }
     const long long len = seq_len(a, b);
-    const float scale = kLog2eF / sqrtf((float)D);
+    const float scale = 1.f / sqrtf((float)D);
     float got = 0.f;
     for (int base = 0; base < n; base += kWRows) {
         __syncthreads();
         stage_rows<float, D, kWThreads>(sm.q, kWRows, q, [&](int r) { return base + r < n ? q + (row0 + base + r) * D : nullptr; });
         if (threadIdx.x < kWRows) {
             const int i = base + threadIdx.x;
-            sm.lse[threadIdx.x] = i < n ? a.lse[row0 + i] * kLog2eF : -INFINITY;
+            sm.lse[threadIdx.x] = i < n ? a.lse[row0 + i] : -INFINITY;
             sm.seen[threadIdx.x] = i < n ? seen_entries(a, len - a.n_q + i / a.heads) : 0;
         }
         tc::cp_async_commit();
@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(SharedArgs a) {
 #pragma unroll
         for (int r = 0; r < kRw; ++r) {
             const float lse = sm.lse[warp * kRw + r];
-            if (e >= 0 && e < sm.seen[warp * kRw + r] && lse != -INFINITY) got += exp2f(fmaf(s[r], scale, -lse));
+            // lse off the logit in one rounding, before the exponent's log2 e (lse log2 e, rounded, costs |lse| 2^-24 of the weight)
+            if (e >= 0 && e < sm.seen[warp * kRw + r] && lse != -INFINITY) got += exp2f(fmaf(s[r], scale, -lse) * kLog2eF);
         }
     }
     sm.sums[warp][lane] = got;

@@ -38,11 +38,11 @@ struct WeightArgs {
     int per_seq, chunks;      // rows of q per sequence, in chunks of up to 256
     int cols, slabs, tiles;   // columns of an MMA (a multiple of 16), d / 64, tiles per item
     int stages, bufs;
-    float scale_log2;
+    float scale;              // 1 / sqrt(d)
 };
 
 struct __align__(16) Shared {
-    float2 col[kMaxCols];     // of a column: -lse log2 e, and the entries that its query sees (as int bits); read in pairs
+    float2 col[kMaxCols];     // of a column: -lse, and the entries that its query sees (as int bits); read in pairs
     uint64_t full[kMaxStages], empty[kMaxStages], d_full[2], d_free[2], drain;
     long long warp_sum[kThreads / 32];
     long long left;
@@ -184,13 +184,14 @@ __device__ void issue(const WeightArgs& c, Shared& sm, uint8_t* ring, uint32_t t
     tc::mbar_wait(&sm.drain, 0);
 }
 
-// this thread's slot against N columns from `c0` on
+// This thread's slot against N columns.  lse is subtracted from the logit in one rounding, before the factor log2 e of the
+// exponent: rounded as lse log2 e it would cost a weight |lse| 2^-24 of its value.
 template <int N>
 __device__ __forceinline__ void add_columns(const float2* col, const uint32_t (&s)[N], float scale, int e, float (&acc)[4]) {
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
         const float4 z = *reinterpret_cast<const float4*>(col + k);
-        const float p0 = exp2f(fmaf(__uint_as_float(s[k]), scale, z.x)), p1 = exp2f(fmaf(__uint_as_float(s[k + 1]), scale, z.z));
+        const float p0 = exp2f(fmaf(__uint_as_float(s[k]), scale, z.x) * kLog2eF), p1 = exp2f(fmaf(__uint_as_float(s[k + 1]), scale, z.z) * kLog2eF);
         acc[k & 3] += e < __float_as_int(z.y) ? p0 : 0.f;
         acc[(k + 1) & 3] += e < __float_as_int(z.w) ? p1 : 0.f;
     }
@@ -226,7 +227,7 @@ __device__ void sum_up(const WeightArgs& c, Shared& sm, uint32_t tmem) {
                     const float lse = a.lse[(long long)b * c.per_seq + row];
                     const long long seen = seen_entries(a, seq_len(a, b) - a.n_q + row / a.heads);
                     if (lse != -INFINITY)
-                        z = make_float2(-lse * kLog2eF, __int_as_float(seen < 0x7fffffff ? (int)seen : 0x7fffffff));
+                        z = make_float2(-lse, __int_as_float(seen < 0x7fffffff ? (int)seen : 0x7fffffff));
                 }
                 sm.col[t256] = z;
                 tc::named_barrier(1, 256);
@@ -241,13 +242,13 @@ __device__ void sum_up(const WeightArgs& c, Shared& sm, uint32_t tmem) {
                     uint32_t s[32];
                     tc::tmem_ld_x32(lanes + buf * 256 + c0, s);
                     tc::tmem_ld_wait();
-                    add_columns<32>(sm.col + c0, s, c.scale_log2, e, acc);
+                    add_columns<32>(sm.col + c0, s, c.scale, e, acc);
                 }
                 if (c0 < c.cols) {
                     uint32_t s[16];
                     tc::tmem_ld_x16(lanes + buf * 256 + c0, s);
                     tc::tmem_ld_wait();
-                    add_columns<16>(sm.col + c0, s, c.scale_log2, e, acc);
+                    add_columns<16>(sm.col + c0, s, c.scale, e, acc);
                 }
                 tc::tc_fence_before();
             }
@@ -340,7 +341,7 @@ cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t st) {
     c.cols = c.per_seq < kMaxCols ? (c.per_seq + 15) / 16 * 16 : kMaxCols;
     c.slabs = a.d / 64;
     c.bufs = c.cols <= kMaxCols / 2 ? 2 : 1;
-    c.scale_log2 = kLog2eF / sqrtf((float)a.d);
+    c.scale = 1.f / sqrtf((float)a.d);
     const long long tiles = (long long)a.batch * ((a.own_rows + kTile - 1) / kTile);
     c.tiles = tiles > 2 * kNumSMs ? 2 : 1;  // few tiles: one per item, so that more blocks have one
     const uint32_t stage = c.tiles * kTileBytes + c.cols * 128;
