@@ -16,6 +16,8 @@ import os
 
 import torch
 
+from .build import binding_tag
+
 __all__ = [
     "V4AError", "F32", "BF16", "FP8E4M3", "MXFP4", "lib", "library_path",
     "v4a_compress", "v4a_compress_dual", "v4a_quantize_mxfp4", "v4a_index_scores", "v4a_index_scores_mxfp4",
@@ -173,6 +175,9 @@ try:
 except ImportError as e:
     raise ImportError(f"the binding module of {_HERE} is not built or was built for another torch ({e}); run "
                       "__graft_entry__.build()") from e
+if getattr(_binding, "built_for", None) != binding_tag():
+    raise ImportError(f"the binding module of {_HERE} was built for {getattr(_binding, 'built_for', 'an unknown torch')}, this is {binding_tag()}; run "
+                      "__graft_entry__.build()")
 
 
 def _check(status: int) -> None:

@@ -59,11 +59,23 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
+def binding_tag() -> str:
+    """What the binding module's compiled code depends on besides its sources: it reads torch's and Python's structures."""
+    import sysconfig
+
+    import torch
+
+    return f"torch {torch.__version__} c++11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}"
+
+
 def build_binding() -> str:
+    tag, stamp = binding_tag(), os.path.join(OBJ, "binding.tag")
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(ROOT, "include", "v4a.h"), os.path.abspath(__file__)]
-    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(d) for d in deps):
-        return BINDING
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(d) for d in deps) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == tag:
+                return BINDING
     import sysconfig
 
     import torch
@@ -74,13 +86,16 @@ def build_binding() -> str:
     includes = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(), os.path.join(cuda, "include"),
                 sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DV4A_BUILT_FOR="{tag}"',
            *[x for i in includes for x in ("-isystem" if i != includes[0] else "-I", i)], src, "-o", BINDING,
            f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
            f"-L{HERE}", "-l:libv4a.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
+    os.makedirs(OBJ, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(tag)
     return BINDING
 
 
