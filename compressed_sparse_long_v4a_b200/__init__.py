@@ -7,7 +7,8 @@ one-line reason when a call returns a non-OK status.  The serving calls, made
 several times a decode step on small inputs, are marshalled by the compiled
 ``_binding`` module instead of through ctypes.  Every step of the
 computation runs in the library's CUDA kernels; there is no other path.  If
-the shared library has not been built, importing this package fails.
+the shared library has not been built, importing this package fails; if
+``_binding`` has not, or was built for another torch, the serving calls do.
 """
 from __future__ import annotations
 
@@ -170,14 +171,31 @@ def _load():
 
 
 lib = _load()
-try:
-    from . import _binding  # the serving calls' marshalling, built beside the library
-except ImportError as e:
-    raise ImportError(f"the binding module of {_HERE} is not built or was built for another torch ({e}); run "
-                      "__graft_entry__.build()") from e
-if getattr(_binding, "built_for", None) != binding_tag():
-    raise ImportError(f"the binding module of {_HERE} was built for {getattr(_binding, 'built_for', 'an unknown torch')}, this is {binding_tag()}; run "
-                      "__graft_entry__.build()")
+
+
+class _Unbuilt:
+    """In the binding module's place where it cannot be used: the serving calls raise why, the others need only the library."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._why}; run __graft_entry__.build()")
+
+
+def _load_binding():
+    """The serving calls' marshalling, built beside the library for one torch and one Python."""
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        return _Unbuilt(f"the binding module of {_HERE} is not built or was built for another torch ({e})")
+    built_for = getattr(b, "built_for", "an unknown torch")
+    if built_for != binding_tag():
+        return _Unbuilt(f"the binding module of {_HERE} was built for {built_for}, this is {binding_tag()}")
+    return b
+
+
+_binding = _load_binding()
 
 
 def _check(status: int) -> None:
