@@ -605,10 +605,10 @@ def v4a_rope(pairs, *, rope_dims: int, positions=None, pos0: int = 0, pos_step: 
 
 def v4a_shared_workspace_size(*, batch: int, n_q: int = 1, heads: int, d: int, n_prefix: int, own_rows: int,
                               window: int = 0, dtype=torch.bfloat16) -> int:
-    """Bytes of workspace for v4a_hca_attend_shared with these sizes."""
+    """Bytes of workspace for v4a_hca_attend_shared with these sizes; 0 for what it rejects."""
     s = _shape(batch, n_q, heads, d, window=window)
     return int(lib.v4a_shared_workspace_size(ctypes.byref(s), int(n_prefix), int(own_rows),
-                                             F32 if dtype == torch.float32 else BF16))
+                                             {torch.float32: F32, torch.bfloat16: BF16}.get(dtype, FP8E4M3)))
 
 
 def v4a_hca_attend_shared(q, prefix, own, ring, out, *, m: int, window: int, ctx_len: int, ctx_lens=None,

@@ -483,6 +483,9 @@ cudaError_t by_shape(const SharedArgs& a, F f) {
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+constexpr int kMaxRows = 0x3fffffff;  // of the prefix, of a sequence's slots, of the window
+bool dims_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+
 // the checks that both calls share; fills everything but the outputs
 v4a_status shared_args(const char* what, const void* q, const v4a_shared_cache* c, v4a_dtype dtype, int* dev_status,
                        const v4a_shape* s, SharedArgs* a) {
@@ -491,13 +494,13 @@ v4a_status shared_args(const char* what, const void* q, const v4a_shared_cache* 
         return report(V4A_ERR_INVALID_ARG, "%s: need batch >= 0, m >= 1, 1 <= n_q <= ctx_len", what);
     if ((long long)s->batch * s->n_q > 65535) return report(V4A_ERR_UNSUPPORTED, "%s: batch * n_q must be <= 65535", what);
     if (s->heads < 1 || s->heads > 1024) return report(V4A_ERR_INVALID_ARG, "%s: heads must be in 1..1024", what);
-    if (s->d != 64 && s->d != 128 && s->d != 256 && s->d != 512)
+    if (!dims_ok(s->d))
         return report(V4A_ERR_UNSUPPORTED, "%s: d must be 64, 128, 256 or 512", what);
     if (dtype != V4A_F32 && dtype != V4A_BF16) return report(V4A_ERR_UNSUPPORTED, "%s: dtype must be F32 or BF16", what);
-    if (c->n_prefix < 0 || c->n_prefix > s->ctx_len / s->m || c->n_prefix > 0x3fffffffLL)
+    if (c->n_prefix < 0 || c->n_prefix > s->ctx_len / s->m || c->n_prefix > kMaxRows)
         return report(V4A_ERR_INVALID_ARG, "%s: n_prefix must be in 0..ctx_len / m", what);
-    if (c->own_rows < 0 || c->own_rows > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: own_rows out of range", what);
-    if (s->window < 0 || s->window > 0x3fffffff) return report(V4A_ERR_INVALID_ARG, "%s: window must be >= 0", what);
+    if (c->own_rows < 0 || c->own_rows > kMaxRows) return report(V4A_ERR_INVALID_ARG, "%s: own_rows out of range", what);
+    if (s->window < 0 || s->window > kMaxRows) return report(V4A_ERR_INVALID_ARG, "%s: window must be >= 0", what);
     if (c->n_prefix + (long long)s->batch * ((long long)c->own_rows + s->window + s->n_q) >= 1LL << 31)
         return report(V4A_ERR_UNSUPPORTED, "%s: n_prefix + batch * (own_rows + window + n_q) must be < 2^31", what);
     if (s->batch > 0 && (!q || (c->own_rows > 0 && !c->own))) return report(V4A_ERR_INVALID_ARG, "%s: q and own are required", what);
@@ -582,9 +585,10 @@ v4a_status v4a_hca_attend_shared(const void* q, const v4a_shared_cache* cache, v
 
 size_t v4a_shared_workspace_size(const v4a_shape* shape, long long n_prefix, int own_rows, v4a_dtype dtype) {
     using namespace v4a;
-    if (!shape || shape->batch < 1 || shape->n_q < 1 || shape->heads < 1 || shape->heads > 1024 || shape->d < 64 ||
-        shape->d > 512 || shape->window < 0 || n_prefix < 0 || own_rows < 0 || (long long)shape->batch * shape->n_q > 65535 ||
-        n_prefix >= 1LL << 31 || n_prefix + (long long)shape->batch * ((long long)own_rows + shape->window + shape->n_q) >= 1LL << 31)
+    if (!shape || shape->batch < 1 || shape->n_q < 1 || (long long)shape->batch * shape->n_q > 65535 || shape->heads < 1 ||
+        shape->heads > 1024 || !dims_ok(shape->d) || (dtype != V4A_F32 && dtype != V4A_BF16) || n_prefix < 0 || n_prefix > kMaxRows ||
+        own_rows < 0 || own_rows > kMaxRows || shape->window < 0 || shape->window > kMaxRows ||
+        n_prefix + (long long)shape->batch * ((long long)own_rows + shape->window + shape->n_q) >= 1LL << 31)
         return 0;
     SharedArgs a = {};
     a.batch = shape->batch;

@@ -216,6 +216,30 @@ def test_shared_workspace_size(v4a):
     assert v4a.v4a_shared_workspace_size(batch=0, heads=64, d=512, n_prefix=1, own_rows=16) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(d=96), dict(d=448), dict(d=1024), dict(heads=1025), dict(batch=65536), dict(window=-1), dict(window=1 << 30),
+                                dict(n_prefix=1 << 30), dict(own_rows=1 << 30), dict(dtype=2), dict(dtype=3), dict(n_q=0)])
+def test_shared_workspace_size_is_0_for_what_the_call_rejects(v4a, kw):
+    f = dict(batch=1, n_q=1, heads=8, d=128, window=0, n_prefix=8, own_rows=16, dtype=1)
+
+    def both(**kw):
+        a = {**f, **kw}
+        s = shape(v4a, batch=a["batch"], n_q=a["n_q"], heads=a["heads"], d=a["d"], window=a["window"], m=1, ctx_len=1 << 40)
+        c = cache(v4a, n_prefix=a["n_prefix"], own_rows=a["own_rows"], ring_rows=(1 << 31) - 1)
+        size = v4a.lib.v4a_shared_workspace_size(ctypes.byref(s), a["n_prefix"], a["own_rows"], a["dtype"])
+        return size, attend(v4a, c, s, dtype=a["dtype"], ws=None)
+
+    assert both()[0] > 0  # and the call, without a workspace, refuses that
+    size, status = both(**kw)
+    assert size == 0 and status in (INVALID, UNSUPPORTED) and b"workspace" not in v4a.lib.v4a_last_error()
+
+
+def test_shared_workspace_size_of_other_dtypes(v4a):
+    import torch
+    f = dict(batch=1, heads=8, d=128, n_prefix=8, own_rows=16)
+    assert v4a.v4a_shared_workspace_size(**f, dtype=torch.float16) == 0
+    assert v4a.v4a_shared_workspace_size(**f, dtype=torch.float32) > 0 and v4a.v4a_shared_workspace_size(**f) > 0
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(lse=None), INVALID), (dict(w_in=None), INVALID), (dict(w_out=None), INVALID), (dict(decay=-1.0), INVALID),
     (dict(decay=float("nan")), INVALID), (dict(w_out=FAKE + 2), INVALID), (dict(dtype=3), UNSUPPORTED), (dict(batch=0), OK)])
