@@ -21,6 +21,7 @@
 #include "internal.h"
 #include "shared.h"
 #include "tc_pair.cuh"
+#include "tensor_map.h"
 #include "turns.h"
 
 #include <type_traits>
@@ -433,8 +434,6 @@ SimtPlan simt_plan(const SharedArgs& a) {
 long long simt_pieces(const SharedArgs& a, const SimtPlan& p) {
     return (long long)p.groups * p.splits + (long long)a.batch * a.n_q * p.head_tiles * p.own_splits;
 }
-
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t simt_bytes(const SharedArgs& a) {
     const long long n = simt_pieces(a, simt_plan(a)) * kRowsB;

@@ -41,12 +41,11 @@
 // softmax and write pieces.
 // Every wait is bounded; on a time-out both CTAs record a device fault, their pieces become NaN and they
 // wind down.  Pieces (m, l, O) are merged by shared_tc_join_kernel: out = sum_i e^{m_i - m} o_i / l.
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
 #include "tc_pair.cuh"
+#include "tensor_map.h"
 #include "turns.h"
 
 namespace v4a {
@@ -870,33 +869,6 @@ __global__ void __launch_bounds__(128) shared_tc_join_kernel(const __grid_consta
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-// [n][rows][512] bf16 viewed as (64 columns, rows, 8 slabs, n); a box is box_rows rows of `slabs` slabs
-bool make_map(CUtensorMap* map, const void* base, long long n, long long rows, int box_rows, int slabs) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[4] = {64, (cuuint64_t)rows, 8, (cuuint64_t)n};
-    cuuint64_t strides[3] = {kD * 2, 128, (cuuint64_t)rows * kD * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)slabs, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
 // everything of the arguments that the sizes alone decide
 void plan(const SharedArgs& a, PairArgs* c) {
     c->a = a;
@@ -987,11 +959,11 @@ cudaError_t launch_shared_tc(const SharedArgs& a, void* ws, cudaStream_t st) {
     if (c.total > 0) {
         const struct { const void* p; long long n, rows; } in[3] = {
             {a.prefix, 1, a.n_prefix}, {a.own, a.batch, a.own_rows}, {a.window > 0 ? a.ring : nullptr, a.batch, a.ring_rows}};
-        bool ok = make_map(&maps.q, a.q, 1, c.rows, kHalf, 8);
+        bool ok = make_slab_map(&maps.q, a.q, 1, c.rows, kD, kHalf, 8);
         for (int k = 0; k < 3; ++k) {
             const bool have = in[k].p && in[k].rows > 0;  // without: no tile asks for it
-            ok = ok && make_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kBox, 4) &&
-                 make_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kBox, 1);
+            ok = ok && make_slab_map(&maps.x[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kD, kBox, 4) &&
+                 make_slab_map(&maps.z[k], have ? in[k].p : a.q, have ? in[k].n : 1, have ? in[k].rows : c.rows, kD, kBox, 1);
         }
         if (!ok) return cudaErrorNotSupported;
         const size_t smem = sizeof(Smem) + 1024;

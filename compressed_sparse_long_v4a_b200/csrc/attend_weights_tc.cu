@@ -16,12 +16,11 @@
 // Warps: 0 loads, 1 issues the MMAs, 2-9 (four per tile) take exponentials and sums, while the next item's
 // products run into the other half of tensor memory (up to 128 columns).  Every wait is bounded; on a
 // time-out the block records a device fault and writes NaN for its items.
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "internal.h"
 #include "shared.h"
 #include "tc_pair.cuh"
+#include "tensor_map.h"
 
 namespace v4a {
 namespace {
@@ -306,31 +305,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
-// [n][rows][d] bf16 viewed as (64 columns, rows, d / 64 slabs, n); a box is box_rows rows of one slab
-bool make_map(CUtensorMap* map, const void* base, long long n, long long rows, int d, int box_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(d / 64), (cuuint64_t)n};
-    cuuint64_t strides[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)rows * d * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t st) {
@@ -348,8 +322,8 @@ cudaError_t launch_weights_tc(const SharedArgs& a, cudaStream_t st) {
     c.stages = (int)(kRing / stage) < kMaxStages ? (int)(kRing / stage) : kMaxStages;
     const size_t smem = (size_t)c.stages * stage + 1024;
     CUtensorMap own_map, q_map;
-    if (!make_map(&own_map, a.own, a.batch, a.own_rows, a.d, kTile) ||
-        !make_map(&q_map, a.q, 1, (long long)a.batch * c.per_seq, a.d, c.cols))
+    if (!make_slab_map(&own_map, a.own, a.batch, a.own_rows, a.d, kTile, 1) ||
+        !make_slab_map(&q_map, a.q, 1, (long long)a.batch * c.per_seq, a.d, c.cols, 1))
         return cudaErrorNotSupported;
     const long long items = (tiles + c.tiles - 1) / c.tiles;
     // the most of any call: host threads share the attribute, and another one may set it before this launch
