@@ -25,12 +25,17 @@
 // Slabs are 64 dims (128 bytes) wide; slab s of the CTA's own keys lies at 8192 s.  CTA 0 has the even slabs
 // of O, CTA 1 the odd ones: block u (16384 u) becomes the 128 keys of slab 2 u + rank.
 //
-// What bounds it: a tile moves about 340 KB through a CTA's shared memory (operands of the MMAs, loads, P) in
-// ~3,200 cycles, 105 of the 128 bytes a cycle, and 96 KB into it from L2, 30 of the 45 bytes a cycle that loads
-// alone reach; the tensor cores are busy 2,100 of those cycles.  Tiles of 64 keys in four stages took 2,300
-// cycles per 64 keys and of 96 in three 1,750, against 1,610.  A piece costs another ~6,000 cycles (128 KB of O per CTA at
-// 32 bytes a cycle).  32 sequences of 64 heads over 8,192 shared entries: 51 us (42 + 9 for the join), 0.68 PFLOP/s, 42% of
-// the measured bf16 peak.
+// What bounds it: two stages, each turned over in a chain of 6,400 cycles (load, S, softmax, O), are a tile in 3,200, of which
+// the tensor cores are busy 2,100; by the counters nothing is saturated (tensor pipe 43%, L1 38%, DRAM 5%).  By count a
+// tile moves 340 KB through a CTA's shared memory (operands of the MMAs, loads, P), which at 128 bytes a cycle would
+// bound it at 2,650, and 96 KB into it from L2, 30 of the 45 bytes a cycle that loads alone reach.  Tiles of 64 keys in
+// four stages took 2,300 cycles per 64 keys and of 96 in three 1,750, against 1,610.  A piece costs another ~6,000 cycles
+// (128 KB of O per CTA at 32 bytes a cycle).  32 sequences of 64 heads over 8,192 shared entries: 51 us (42 + 9 for the join),
+// 0.68 PFLOP/s, 42% of the measured bf16 peak.
+//
+// The ranges are cut by what the caches have room for, since the host does not know the counts: where they hold less, the
+// pairs with the prefix have more to do than the others.  The same with 64 own slots filled per sequence: 45 us in caches of 64,
+// 51 in 1,024, 67 in 4,096, 91 in 8,192.
 //
 // Masked places may hold anything.  A NaN or infinity in a row of K = V makes the raw S of every row of the
 // matrix non-finite at that key, so the softmax threads see it, also for rows that do not see the
@@ -239,7 +244,7 @@ __device__ __forceinline__ bool aborted(Smem& sm) { return *reinterpret_cast<vol
 
 // ---------------------------------------------------------------------
 // warp 0, one lane: finds the tiles, tells the other warps of this CTA about them, and loads the queries and this CTA's
-// 32 keys.  Both CTAs' copies complete on CTA 0's barriers, which expect the bytes of both.
+// 64 keys.  Both CTAs' copies complete on CTA 0's barriers, which expect the bytes of both.
 // ---------------------------------------------------------------------
 struct Maps {
     CUtensorMap x[3], z[3], q;  // by Kind: 64 rows x 4 slabs; 64 rows x 1 slab
@@ -338,7 +343,7 @@ __device__ void load_x(Smem& sm, const PairArgs& c, const Maps& maps, int pair, 
     }
 }
 
-// warp 10, one lane: the other CTA's 32 keys of this CTA's slabs, once S has been computed
+// warp 10, one lane: the other CTA's 64 keys of this CTA's slabs, once S has been computed
 __device__ void load_z(Smem& sm, const PairArgs& c, const Maps& maps, uint32_t rank) {
     const uint64_t again = tc::l2_evict_normal();
     const uint32_t other = rank ^ 1;
@@ -596,6 +601,9 @@ __device__ void softmax(Smem& sm, const PairArgs& c, uint32_t tmem, int pair, ui
                 for (int k = 0; k < 16; ++k) {
                     const float p0 = exp2_fast(fmaf(x[2 * k], c.scale_log2, -sub_m)), p1 = exp2_fast(fmaf(x[2 * k + 1], c.scale_log2, -sub_m));
                     ls[k & 1] += p0 + p1;  // the sum is of the unrounded weights
+                    // To V's type, which the tensor cores multiply it with: off by up to 2^-8 of itself, also for fp32 outputs (two
+                    // bf16 parts would double the products of O).  The outputs' error against 64 bits is 1.8e-3 to 2.0e-3 with it,
+                    // relative, as bf16 outputs, 1.65e-3 without.
                     const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
                     pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
                 }
