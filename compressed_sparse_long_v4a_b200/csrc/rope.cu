@@ -10,7 +10,8 @@
 // the angles are read again for every row.  Measured: 4,096 tokens of 64 x 512 bf16 89.6 us, 6.1 TB/s, 93% of the measured copy
 // bandwidth (an index per item and a barrier per token took 267 us); 16,000 tokens of (8 + 1) x 512 and 4 x 128 65 us, 5.1 TB/s
 // (a token per block: 102 us), half pairs 69 us; 1,554 of 17 x 128 fp32, half pairs, 7.6 us; a decode step of four tokens 3.1 us on the
-// device.  4,096 tokens of 65 x 512 bf16: 88 us, half pairs 118; in rows of 513 (any alignment, an element at a time) 322 us.  With few tokens (a decode step) a token's heads are cut over blocks.
+// device.  4,096 tokens of 65 x 512 bf16: 88 us, half pairs 118; in place 21 and 18; in rows of 513 (any alignment, an element
+// at a time) 322 us, in place 42.  With few tokens (a decode step) a token's heads are cut over blocks.
 #include "common.cuh"
 #include "internal.h"
 #include "turns.h"
